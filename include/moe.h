@@ -344,6 +344,138 @@ MOE_API moe_status moe_backward(const moe_config *cfg, const void *x, const void
                                 const void *ws, size_t ws_bytes, void *bws, size_t bws_bytes,
                                 moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Dense operators beside the MoE layer.  "An MoE layer replaces every other
+ * FFN" (GShard section 3): the entry points below are the FFNs in between,
+ * the residual that the layer leaves to the caller, and the clipping of a
+ * training step's gradients.
+ *
+ * They follow the conventions at the top of this file (asynchronous, host
+ * validation before any launch, caller's workspace, no allocation), with
+ * these differences:
+ *   - any size: rows (tokens) may be 0, widths need not be multiples of
+ *     anything;
+ *   - tensors of rows take a row stride ld in elements (0: packed, the row
+ *     width), and every pointer needs the alignment of its element type
+ *     only.  Rows whose base address and stride are multiples of 16 bytes
+ *     are read fastest;
+ *   - biases, residuals and gradients have the layer's dtype.  Sums are held
+ *     in fp32 and each output is rounded once; the intermediate matrices
+ *     that a second product reads (h; in the backward passes dz, dA, dU and
+ *     the remade h) are rounded to the layer's dtype first;
+ *   - outputs may not overlap inputs or one another, except that y may be
+ *     the residual itself (same address and stride).  Column slices of one
+ *     wider buffer do not overlap.
+ * ------------------------------------------------------------------------- */
+typedef enum moe_dense_act {
+  MOE_DENSE_IDENTITY = 0,
+  MOE_DENSE_RELU = 1,
+  MOE_DENSE_SILU = 2,      /* v / (1 + e^-v)                                         */
+  MOE_DENSE_GELU = 3,      /* v Phi(v), Phi the normal distribution function (erf)   */
+  MOE_DENSE_GELU_TANH = 4  /* v / 2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3)))        */
+} moe_dense_act;
+
+/* y = act(x W^T + b) + r:  x [M, K], w [N, K], b [N], r and y [M, N]. */
+typedef struct moe_linear_config {
+  int64_t M;       /* rows (>= 0)                                                     */
+  int32_t K, N;    /* input and output width (>= 1)                                   */
+  int32_t act;     /* moe_dense_act                                                   */
+  int32_t dtype;   /* moe_dtype                                                       */
+  int64_t ld_x;    /* row stride of x and dx (0: K)                                   */
+  int64_t ld_w;    /* row stride of w (0: K); dw is packed                            */
+  int64_t ld_r;    /* row stride of the residual (0: N)                               */
+  int64_t ld_y;    /* row stride of y and dy (0: N)                                   */
+  int64_t reserved;/* 0                                                               */
+} moe_linear_config;
+
+/* Bytes of workspace of moe_linear (backward = 0) or moe_linear_backward (1). */
+MOE_API moe_status moe_query_linear_size(const moe_linear_config *cfg, int32_t backward, size_t *bytes);
+
+/* z = x W^T + b;  y = act(z) + r.  bias, residual and z may be NULL; z [M, N]
+ * (packed) receives the pre-activations for the backward pass. */
+MOE_API moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *w, const void *bias,
+                              const void *residual, void *y, void *z, void *ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* dz = dy * act'(z);  dx = dz W,  dw = dz^T x,  dbias[n] = sum_m dz[m, n].
+ * (The residual's gradient is dy itself.)  z: as moe_linear wrote it; not
+ * read, and may be NULL, with MOE_DENSE_IDENTITY.  dx [M, K], dw [N, K]
+ * (packed), dbias [N] are overwritten; each may be NULL (not computed), not
+ * all three.  relu'(0) = 0.  M = 0 gives zero dw and dbias. */
+MOE_API moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, const void *w,
+                                       const void *z, const void *dy, void *dx, void *dw, void *dbias,
+                                       void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gated feed-forward block (SwiGLU with MOE_DENSE_SILU: one expert of the
+ * layer's FFN, without a gate):
+ *   a = x W1^T + b1, u = x W3^T + b3, h = act(a) * u, y = h W2^T + b2 + r
+ * x, r, y [T, d]; w1, w3 [f, d] and w2 [d, f] packed; b1, b3 [f], b2 [d]. */
+typedef struct moe_gated_ffn_config {
+  int64_t T;        /* rows (>= 0)                                                    */
+  int32_t d_model;  /* d (>= 1)                                                       */
+  int32_t d_ff;     /* f (>= 1)                                                       */
+  int32_t act;      /* moe_dense_act                                                  */
+  int32_t dtype;    /* moe_dtype                                                      */
+  int64_t ld_x;     /* row stride of x and dx (0: d)                                  */
+  int64_t ld_r;     /* row stride of the residual (0: d)                              */
+  int64_t ld_y;     /* row stride of y and dy (0: d)                                  */
+  int64_t reserved; /* 0                                                              */
+} moe_gated_ffn_config;
+
+MOE_API moe_status moe_query_gated_ffn_size(const moe_gated_ffn_config *cfg, int32_t backward, size_t *bytes);
+
+/* b1 and b3 (both or neither), b2 and residual may be NULL.  a and u [T, f]
+ * (packed; both or neither) receive the pre-activations for the backward
+ * pass.  Both projections, the activation and the product run in one kernel;
+ * h lives in the workspace, in the layer's dtype. */
+MOE_API moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const void *w1,
+                                 const void *b1, const void *w3, const void *b3, const void *w2,
+                                 const void *b2, const void *residual, void *y, void *a, void *u, void *ws,
+                                 size_t ws_bytes, moe_stream_t stream);
+
+/* Gradients of sum(dy * y) from x, the weights and the a, u of the forward:
+ *   dh = dy W2,  dA = dh * u * act'(a),  dU = dh * act(a),  h = act(a) * u
+ *   dx = dA W1 + dU W3,  dw1 = dA^T x,  dw3 = dU^T x,  dw2 = dy^T h,
+ *   db1, db3, db2: the column sums of dA, dU and dy
+ * (the residual's gradient is dy itself).  Every output is overwritten and
+ * may be NULL (not computed), not all of them; dw1 and dw3, db1 and db3 go
+ * together. */
+MOE_API moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x, const void *w1,
+                                          const void *w3, const void *w2, const void *a, const void *u,
+                                          const void *dy, void *dx, void *dw1, void *db1, void *dw3,
+                                          void *db3, void *dw2, void *db2, void *ws, size_t ws_bytes,
+                                          moe_stream_t stream);
+
+/* One gradient of a list: n contiguous elements of dtype at src (read) and
+ * dst (written by moe_clip_grads; dst == src clips in place). */
+typedef struct moe_grad {
+  const void *src;
+  void *dst;
+  int64_t n;        /* >= 0                                                            */
+  int32_t dtype;    /* moe_dtype; a list may mix them                                  */
+  int32_t reserved; /* 0                                                               */
+} moe_grad;
+
+/* Bytes of workspace of moe_grad_norm and moe_clip_grads for `count` tensors. */
+MOE_API moe_status moe_query_clip_size(int32_t count, size_t *bytes);
+
+/* norm[0] (fp32, device) = sqrt of the sum of squares over all `count`
+ * tensors of the list (host array, read before the call returns; dst is
+ * ignored).  Squares and sums in fp64, in a fixed order: the same bits on
+ * every call.  An empty list has norm 0. */
+MOE_API moe_status moe_grad_norm(const moe_grad *grads, int32_t count, float *norm, void *ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/* The same norm, then dst = c * src with c = min(1, max_norm / (norm + 1e-6))
+ * in fp32 (one rounding to the tensor's dtype).  max_norm > 0 (infinity: c =
+ * 1 whatever the norm).  No host sync: c is computed on the device.  An
+ * infinite element makes the norm infinite and c = 0 (then inf * 0 = NaN in
+ * that place), a NaN makes every result NaN; norm shows it.  norm may be
+ * NULL.  No two of the tensors written may overlap, nor one written and
+ * another read (a tensor listed twice: MOE_ERR_INVALID_ARG). */
+MOE_API moe_status moe_clip_grads(const moe_grad *grads, int32_t count, float max_norm, float *norm, void *ws,
+                                  size_t ws_bytes, moe_stream_t stream);
+
 /* Waits for `stream`, then reads and clears the workspace's device error
  * word.  Returns MOE_OK, MOE_ERR_TIMEOUT or MOE_ERR_DEVICE_CHECK; *flags (if
  * not NULL) receives the raw bits.  After an error it also clears the rest

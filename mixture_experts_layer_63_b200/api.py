@@ -26,13 +26,17 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_ACT_RELU, MOE_ACT_SWIGLU = 0, 1
 MOE_TOKEN_CHOICE, MOE_EXPERT_CHOICE = 0, 1
 MOE_ROUTE_SOFTMAX, MOE_ROUTE_BIAS, MOE_ROUTE_LOAD = 0, 1, 2
+DENSE_ACTS = {"identity": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}    # moe_dense_act
 ROUTE_RULES = {"softmax": MOE_ROUTE_SOFTMAX, "bias": MOE_ROUTE_BIAS, "load": MOE_ROUTE_LOAD}
 
 EXPORTS = ("moe_query_sizes", "moe_route", "moe_gate", "moe_permute", "moe_expert_ffn",
            "moe_combine", "moe_forward", "moe_check_device_errors", "moe_workspace_init",
            "moe_status_string", "moe_permute_noalloc", "moe_forward_timed",
            "moe_route_bias_update", "moe_query_backward_size", "moe_backward",
-           "moe_kernel_launches", "moe_workspace_set_wait_limit", "moe_forward_host")
+           "moe_kernel_launches", "moe_workspace_set_wait_limit", "moe_forward_host",
+           "moe_query_linear_size", "moe_linear", "moe_linear_backward",
+           "moe_query_gated_ffn_size", "moe_gated_ffn", "moe_gated_ffn_backward",
+           "moe_query_clip_size", "moe_grad_norm", "moe_clip_grads")
 
 
 class MoeError(RuntimeError):
@@ -58,6 +62,24 @@ class MoeSizes(ctypes.Structure):
                 ("tok_rows_len", ctypes.c_int64), ("step_workspace", ctypes.c_size_t),
                 ("workspace", ctypes.c_size_t), ("capacity", ctypes.c_int64),
                 ("permute_workspace", ctypes.c_size_t), ("host_workspace", ctypes.c_size_t)]
+
+
+class MoeLinearConfig(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("ld_x", ctypes.c_int64),
+                ("ld_w", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("reserved", ctypes.c_int64)]
+
+
+class MoeGatedFfnConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d_model", ctypes.c_int32), ("d_ff", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("ld_x", ctypes.c_int64),
+                ("ld_r", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("reserved", ctypes.c_int64)]
+
+
+class MoeGrad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -90,6 +112,17 @@ def lib() -> ctypes.CDLL:
             "moe_check_device_errors": [vp, sz, vp, ctypes.POINTER(ctypes.c_uint32)],
             "moe_workspace_init": [vp, sz, vp],
             "moe_workspace_set_wait_limit": [vp, sz, ctypes.c_uint64, vp],
+            "moe_query_linear_size": [ctypes.POINTER(MoeLinearConfig), ctypes.c_int32,
+                                      ctypes.POINTER(sz)],
+            "moe_linear": [ctypes.POINTER(MoeLinearConfig)] + [vp] * 7 + [sz, vp],
+            "moe_linear_backward": [ctypes.POINTER(MoeLinearConfig)] + [vp] * 8 + [sz, vp],
+            "moe_query_gated_ffn_size": [ctypes.POINTER(MoeGatedFfnConfig), ctypes.c_int32,
+                                         ctypes.POINTER(sz)],
+            "moe_gated_ffn": [ctypes.POINTER(MoeGatedFfnConfig)] + [vp] * 12 + [sz, vp],
+            "moe_gated_ffn_backward": [ctypes.POINTER(MoeGatedFfnConfig)] + [vp] * 15 + [sz, vp],
+            "moe_query_clip_size": [ctypes.c_int32, ctypes.POINTER(sz)],
+            "moe_grad_norm": [ctypes.POINTER(MoeGrad), ctypes.c_int32, vp, vp, sz, vp],
+            "moe_clip_grads": [ctypes.POINTER(MoeGrad), ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -541,3 +574,240 @@ def moe_permute_noalloc(cfg, x, topk_idx, topk_gate, probs, counts, offsets, tok
         ctypes.byref(cfg), _ptr(x, n.td, n.dt), _ptr(topk_idx), _ptr(topk_gate), _ptr(probs),
         *_permute_outputs(n, counts, offsets, tok_rows, row_token, row_gate, x_perm, n_dropped),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# dense operators beside the layer: linear, gated feed-forward block, clipping
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _moe_dtype(dtype: torch.dtype) -> int:
+    if dtype not in _DTYPES:
+        raise ValueError(f"expected torch.float32 or torch.bfloat16, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _on_device(t: torch.Tensor) -> None:
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only (no CPU path)")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor | None, rows: int, width: int, ld: int, dtype: int):
+    """Device pointer of a [rows, width] tensor whose rows are `ld` elements
+    apart (0: packed) and contiguous within themselves."""
+    if t is None:
+        return None
+    _on_device(t)
+    if _DTYPES.get(t.dtype) != dtype:
+        raise ValueError(f"{t.dtype} tensor, but the configuration's dtype is another")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"expected [{rows}, {width}], got {list(t.shape)}")
+    if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or width)):
+        raise ValueError(f"strides {t.stride()}, but the configuration's rows are {ld or width} apart")
+    return t.data_ptr()
+
+
+def _vec(t: torch.Tensor | None, n: int, dtype: int):
+    """Device pointer of a contiguous vector of n elements."""
+    if t is None:
+        return None
+    return _rows(t.view(1, -1) if t.dim() == 1 else t, 1, n, 0, dtype)
+
+
+def linear_config(M: int, K: int, N: int, act: str = "identity", dtype: torch.dtype = torch.bfloat16,
+                  ld_x: int = 0, ld_w: int = 0, ld_r: int = 0, ld_y: int = 0) -> MoeLinearConfig:
+    """y [M, N] = act(x [M, K] w [N, K]^T + b) + r; ld_*: row strides in elements (0: packed)."""
+    if act not in DENSE_ACTS:
+        raise ValueError(f"act is one of {', '.join(DENSE_ACTS)}, got {act!r}")
+    return MoeLinearConfig(M, K, N, DENSE_ACTS[act], _moe_dtype(dtype), ld_x, ld_w, ld_r, ld_y, 0)
+
+
+def gated_ffn_config(T: int, d_model: int, d_ff: int, act: str = "silu",
+                     dtype: torch.dtype = torch.bfloat16, ld_x: int = 0, ld_y: int = 0,
+                     ld_r: int = 0) -> MoeGatedFfnConfig:
+    """y [T, d] = (act(x w1^T + b1) * (x w3^T + b3)) w2^T + b2 + r; ld_*: row strides (0: packed)."""
+    if act not in DENSE_ACTS:
+        raise ValueError(f"act is one of {', '.join(DENSE_ACTS)}, got {act!r}")
+    return MoeGatedFfnConfig(T, d_model, d_ff, DENSE_ACTS[act], _moe_dtype(dtype), ld_x, ld_r, ld_y, 0)
+
+
+def _query(fn: str, *args) -> int:
+    out = ctypes.c_size_t(0)
+    _check(fn, getattr(lib(), fn)(*args, ctypes.byref(out)))
+    return out.value
+
+
+def _dense_workspace(nbytes: int, device) -> torch.Tensor:
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:4096].zero_()                       # the control block
+    return ws
+
+
+def new_linear_workspace(cfg: MoeLinearConfig, backward: bool = False, device="cuda") -> torch.Tensor:
+    """A workspace of the size moe_linear (or moe_linear_backward) needs."""
+    return _dense_workspace(_query("moe_query_linear_size", ctypes.byref(cfg), int(backward)), device)
+
+
+def new_gated_ffn_workspace(cfg: MoeGatedFfnConfig, backward: bool = False, device="cuda") -> torch.Tensor:
+    """A workspace of the size moe_gated_ffn (or moe_gated_ffn_backward) needs."""
+    return _dense_workspace(_query("moe_query_gated_ffn_size", ctypes.byref(cfg), int(backward)), device)
+
+
+def moe_linear(cfg, x, w, bias, residual, y, z, ws, stream=None):
+    """y = act(x w^T + bias) + residual; z (or None) receives x w^T + bias."""
+    wp, wn = _ws(ws)
+    c, dt = cfg, cfg.dtype
+    _check("moe_linear", lib().moe_linear(
+        ctypes.byref(c), _rows(x, c.M, c.K, c.ld_x, dt), _rows(w, c.N, c.K, c.ld_w, dt), _vec(bias, c.N, dt),
+        _rows(residual, c.M, c.N, c.ld_r, dt), _rows(y, c.M, c.N, c.ld_y, dt), _rows(z, c.M, c.N, 0, dt),
+        wp, wn, _stream(stream)))
+
+
+def moe_linear_backward(cfg, x, w, z, dy, dx, dw, dbias, ws, stream=None):
+    """Gradients of sum(dy * y): dx, dw, dbias (each may be None)."""
+    wp, wn = _ws(ws)
+    c, dt = cfg, cfg.dtype
+    _check("moe_linear_backward", lib().moe_linear_backward(
+        ctypes.byref(c), _rows(x, c.M, c.K, c.ld_x, dt), _rows(w, c.N, c.K, c.ld_w, dt),
+        _rows(z, c.M, c.N, 0, dt), _rows(dy, c.M, c.N, c.ld_y, dt), _rows(dx, c.M, c.K, c.ld_x, dt),
+        _rows(dw, c.N, c.K, 0, dt), _vec(dbias, c.N, dt), wp, wn, _stream(stream)))
+
+
+def moe_gated_ffn(cfg, x, w1, b1, w3, b3, w2, b2, residual, y, a, u, ws, stream=None):
+    """y = (act(x w1^T + b1) * (x w3^T + b3)) w2^T + b2 + residual; a, u (or
+    None) receive the two pre-activations for the backward pass."""
+    wp, wn = _ws(ws)
+    T, d, f, dt = cfg.T, cfg.d_model, cfg.d_ff, cfg.dtype
+    _check("moe_gated_ffn", lib().moe_gated_ffn(
+        ctypes.byref(cfg), _rows(x, T, d, cfg.ld_x, dt), _rows(w1, f, d, 0, dt), _vec(b1, f, dt),
+        _rows(w3, f, d, 0, dt), _vec(b3, f, dt), _rows(w2, d, f, 0, dt), _vec(b2, d, dt),
+        _rows(residual, T, d, cfg.ld_r, dt), _rows(y, T, d, cfg.ld_y, dt), _rows(a, T, f, 0, dt),
+        _rows(u, T, f, 0, dt), wp, wn, _stream(stream)))
+
+
+def moe_gated_ffn_backward(cfg, x, w1, w3, w2, a, u, dy, dx, dw1, db1, dw3, db3, dw2, db2, ws, stream=None):
+    """Gradients of sum(dy * y) from the forward's a and u (outputs may be None)."""
+    wp, wn = _ws(ws)
+    T, d, f, dt = cfg.T, cfg.d_model, cfg.d_ff, cfg.dtype
+    _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
+        ctypes.byref(cfg), _rows(x, T, d, cfg.ld_x, dt), _rows(w1, f, d, 0, dt), _rows(w3, f, d, 0, dt),
+        _rows(w2, d, f, 0, dt), _rows(a, T, f, 0, dt), _rows(u, T, f, 0, dt), _rows(dy, T, d, cfg.ld_y, dt),
+        _rows(dx, T, d, cfg.ld_x, dt), _rows(dw1, f, d, 0, dt), _vec(db1, f, dt), _rows(dw3, f, d, 0, dt),
+        _vec(db3, f, dt), _rows(dw2, d, f, 0, dt), _vec(db2, d, dt), wp, wn, _stream(stream)))
+
+
+def _grad_list(grads, out=None):
+    """The C list of a sequence of contiguous CUDA tensors (None entries are skipped)."""
+    pairs = [(g, o) for g, o in zip(grads, out if out is not None else grads, strict=True) if g is not None]
+    arr = (MoeGrad * max(1, len(pairs)))()
+    for e, (g, o) in zip(arr, pairs):
+        _on_device(g)
+        if not g.is_contiguous():
+            raise ValueError("libmoe takes contiguous gradients")
+        if o is not g:
+            _on_device(o)
+            if not o.is_contiguous() or o.dtype != g.dtype or o.numel() != g.numel():
+                raise ValueError("each output is a contiguous tensor of its gradient's size and dtype")
+        e.src, e.dst, e.n, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _moe_dtype(g.dtype)
+    return arr, len(pairs)
+
+
+def new_clip_workspace(grads, device="cuda") -> torch.Tensor:
+    """A workspace for moe_grad_norm / moe_clip_grads on a list of this length."""
+    return _dense_workspace(_query("moe_query_clip_size", len(grads)), device)
+
+
+def moe_grad_norm(grads, norm, ws, stream=None):
+    """norm (one fp32 element) = sqrt of the sum of squares over all tensors of the list."""
+    arr, n = _grad_list(grads)
+    wp, wn = _ws(ws)
+    _check("moe_grad_norm", lib().moe_grad_norm(arr, n, _ptr(norm, 1, torch.float32), wp, wn,
+                                                _stream(stream)))
+
+
+def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
+    """Scale every tensor of the list by min(1, max_norm / (norm + 1e-6)), in
+    place or into the tensors of `out`; norm (or None) receives the norm
+    before clipping."""
+    arr, n = _grad_list(grads, out)
+    wp, wn = _ws(ws)
+    _check("moe_clip_grads", lib().moe_clip_grads(arr, n, float(max_norm), _ptr(norm, 1, torch.float32), wp, wn,
+                                                  _stream(stream)))
+
+
+class GatedFFN:
+    """A dense gated feed-forward block between MoE layers: its weights and
+    workspaces.  ``block(x, residual)`` runs moe_gated_ffn on any number of
+    rows; with ``train=True`` it keeps the pre-activations for
+    ``block.backward(x, dy)``.  Workspaces grow with the largest batch seen;
+    calls of one object share them, so keep them on one stream."""
+
+    def __init__(self, w1, w3, w2, b1=None, b3=None, b2=None, act: str = "silu"):
+        self.w1, self.w3, self.w2, self.b1, self.b3, self.b2, self.act = w1, w3, w2, b1, b3, b2, act
+        self.ws = self.bws = None
+        self.a = self.u = None
+        self.cfgs: dict[tuple, MoeGatedFfnConfig] = {}
+
+    def _cfg(self, x, y, residual=None) -> MoeGatedFfnConfig:
+        ld = [0 if t is None or t.shape[0] < 2 else t.stride(0) for t in (x, y, residual)]
+        key = (x.shape[0], *ld)
+        c = self.cfgs.get(key)
+        if c is None:
+            c = gated_ffn_config(x.shape[0], self.w1.shape[1], self.w1.shape[0], self.act, self.w1.dtype, *ld)
+            if len(self.cfgs) < 256:
+                self.cfgs[key] = c
+        return c
+
+    def _room(self, ws, cfg, backward: bool):
+        need = _query("moe_query_gated_ffn_size", ctypes.byref(cfg), int(backward))
+        return ws if ws is not None and ws.numel() >= need else _dense_workspace(need, self.w1.device)
+
+    def __call__(self, x, residual=None, out=None, train: bool = False, stream=None):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        cfg = self._cfg(x, y, residual)
+        self.ws = self._room(self.ws, cfg, False)
+        if train:
+            self.a = torch.empty(x.shape[0], self.w1.shape[0], dtype=x.dtype, device=x.device)
+            self.u = torch.empty_like(self.a)
+        moe_gated_ffn(cfg, x, self.w1, self.b1, self.w3, self.b3, self.w2, self.b2, residual, y,
+                      self.a if train else None, self.u if train else None, self.ws, stream)
+        return y
+
+    def backward(self, x, dy, stream=None) -> dict:
+        """Gradients of sum(dy * y) for the last ``self(x, train=True)`` (same
+        x): dx, dw1, dw3, dw2 and, with biases, db1, db3, db2, in the layer's
+        dtype.  The residual's gradient is dy."""
+        if self.a is None or self.a.shape[0] != x.shape[0]:
+            raise ValueError("backward follows a forward with train=True on the same x")
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        g = {"dx": dx}
+        for p in ("w1", "w3", "w2", "b1", "b3", "b2"):
+            t = getattr(self, p)
+            g["d" + p] = torch.empty_like(t) if t is not None else None
+        T = x.shape[0]
+        # dx is packed here: the strided x of the configuration would also be dx's
+        xc = x if T < 2 or x.stride(0) == x.shape[1] else x.contiguous()
+        cfg = self._cfg(xc, dy)
+        self.bws = self._room(self.bws, cfg, True)
+        moe_gated_ffn_backward(cfg, xc, self.w1, self.w3, self.w2, self.a, self.u, dy, dx, g["dw1"], g["db1"],
+                               g["dw3"], g["db3"], g["dw2"], g["db2"], self.bws, stream)
+        return g
+
+
+def clip_grads(grads, max_norm: float, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Clip one training step's gradients in place by their global norm:
+    `grads` is a list of tensors and of the dicts that MoELayer.backward and
+    GatedFFN.backward return (their dx, which belongs to the layer below, is
+    left out).  Returns the norm before clipping (one fp32 element on the GPU)."""
+    flat = []
+    for g in grads:
+        flat += [t for k, t in g.items() if k != "dx"] if isinstance(g, dict) else [g]
+    flat = [t for t in flat if t is not None]
+    norm = torch.empty((), dtype=torch.float32, device="cuda")
+    moe_clip_grads(flat, max_norm, norm, ws if ws is not None else new_clip_workspace(flat), stream=stream)
+    return norm

@@ -1,0 +1,492 @@
+// C ABI of the dense operators (declared in include/moe.h): argument
+// validation, workspace layout and the launch sequence of each entry point.
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "dense_internal.h"
+
+namespace moe {
+namespace {
+
+struct DenseRange {
+  explicit DenseRange(const char *name) { nvtxRangePushA(name); }
+  ~DenseRange() { nvtxRangePop(); }
+  DenseRange(const DenseRange &) = delete;
+  DenseRange &operator=(const DenseRange &) = delete;
+};
+
+constexpr int64_t kMaxRows = 0x7fffffff;
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Workspace: pieces of the caller's buffer, one after another.
+struct Taker {
+  size_t o = align256(kCtrlBytes);
+  size_t take(size_t bytes) {
+    const size_t at = o;
+    o = align256(o + bytes);
+    return at;
+  }
+};
+
+// ---- memory spans -------------------------------------------------------------
+// `rows` rows of `width` elements, `ld` apart
+struct Span {
+  const void *p;
+  int64_t rows, width, ld;
+  int es;
+  uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
+  uintptr_t end() const { return begin() + (uintptr_t)((rows - 1) * ld + width) * es; }
+  bool none() const { return !p || rows == 0; }
+};
+
+bool overlap(const Span &a, const Span &b) {
+  if (a.none() || b.none() || a.end() <= b.begin() || b.end() <= a.begin()) return false;
+  // column slices of one buffer: the same row stride, no common column
+  if (a.ld == b.ld && a.es == b.es && a.rows > 1 && b.rows > 1) {
+    const Span &lo = a.begin() <= b.begin() ? a : b, &hi = a.begin() <= b.begin() ? b : a;
+    const uintptr_t gap = hi.begin() - lo.begin(), row = (uintptr_t)a.ld * a.es;
+    const uintptr_t col = gap % row;
+    if (col >= (uintptr_t)lo.width * a.es && col + (uintptr_t)hi.width * a.es <= row) return false;
+  }
+  return true;
+}
+
+bool aligned_to(const void *p, int es) { return !p || reinterpret_cast<uintptr_t>(p) % es == 0; }
+
+// outputs against inputs and one another; every pointer aligned to its element
+moe_status check_spans(const std::initializer_list<Span> &in, const std::initializer_list<Span> &out) {
+  for (const Span &s : in)
+    if (!aligned_to(s.p, s.es)) return MOE_ERR_INVALID_ARG;
+  for (const Span *o = out.begin(); o != out.end(); ++o) {
+    if (!aligned_to(o->p, o->es)) return MOE_ERR_INVALID_ARG;
+    for (const Span &s : in)
+      if (overlap(*o, s)) return MOE_ERR_INVALID_ARG;
+    for (const Span *q = out.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+moe_status check_dense_ws(const void *ws, size_t ws_bytes, size_t need) {
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+moe_status dense_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+bool bad_ld(int64_t ld, int64_t width) { return ld != 0 && (ld < width || ld > kMaxRows); }
+
+moe_status validate_act(int32_t act, int32_t dtype) {
+  if (act < MOE_DENSE_IDENTITY || act > MOE_DENSE_GELU_TANH) return MOE_ERR_INVALID_ARG;
+  return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+// ---- linear ---------------------------------------------------------------------
+moe_status validate_linear(const moe_linear_config *in, moe_linear_config *c) {
+  if (!in) return MOE_ERR_INVALID_ARG;
+  *c = *in;
+  if (c->M < 0 || c->K < 1 || c->N < 1 || c->reserved != 0) return MOE_ERR_INVALID_ARG;
+  const moe_status st = validate_act(c->act, c->dtype);
+  if (st != MOE_OK) return st;
+  if (bad_ld(c->ld_x, c->K) || bad_ld(c->ld_w, c->K) || bad_ld(c->ld_r, c->N) || bad_ld(c->ld_y, c->N))
+    return MOE_ERR_INVALID_ARG;
+  if (c->M > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (c->ld_x == 0) c->ld_x = c->K;
+  if (c->ld_w == 0) c->ld_w = c->K;
+  if (c->ld_r == 0) c->ld_r = c->N;
+  if (c->ld_y == 0) c->ld_y = c->N;
+  return MOE_OK;
+}
+
+struct LinearLayout {
+  size_t dz, part, total;
+};
+
+LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
+  LinearLayout L{};
+  Taker t;
+  if (backward) {
+    L.dz = t.take(c.act != MOE_DENSE_IDENTITY ? (size_t)c.M * c.N * dense_elem(c.dtype) : 0);
+    L.part = t.take(colsum_scratch(c.M, c.N));
+  }
+  L.total = t.o;
+  return L;
+}
+
+cudaError_t run_product(const DenseGemm &g, cudaStream_t s) { return launch_dense_simt(g, s); }
+
+// ---- gated block ------------------------------------------------------------------
+moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *c) {
+  if (!in) return MOE_ERR_INVALID_ARG;
+  *c = *in;
+  if (c->T < 0 || c->d_model < 1 || c->d_ff < 1 || c->reserved != 0) return MOE_ERR_INVALID_ARG;
+  const moe_status st = validate_act(c->act, c->dtype);
+  if (st != MOE_OK) return st;
+  if (bad_ld(c->ld_x, c->d_model) || bad_ld(c->ld_r, c->d_model) || bad_ld(c->ld_y, c->d_model))
+    return MOE_ERR_INVALID_ARG;
+  if (c->T > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (c->ld_x == 0) c->ld_x = c->d_model;
+  if (c->ld_r == 0) c->ld_r = c->d_model;
+  if (c->ld_y == 0) c->ld_y = c->d_model;
+  return MOE_OK;
+}
+
+struct GatedLayout {
+  size_t h, da, du, part, total;
+};
+
+GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
+  GatedLayout L{};
+  Taker t;
+  const size_t tf = (size_t)c.T * c.d_ff * dense_elem(c.dtype);
+  L.h = t.take(tf);
+  if (backward) {
+    L.da = t.take(tf);
+    L.du = t.take(tf);
+    L.part = t.take(colsum_scratch(c.T, std::max(c.d_ff, c.d_model)));
+  }
+  L.total = t.o;
+  return L;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_query_linear_size(const moe_linear_config *cfg, int32_t backward, size_t *bytes) {
+  moe_linear_config c;
+  if (!bytes || (backward != 0 && backward != 1)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = validate_linear(cfg, &c);
+  if (st == MOE_OK) *bytes = linear_layout(c, backward != 0).total;
+  return st;
+}
+
+moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *w, const void *bias,
+                      const void *residual, void *y, void *z, void *ws, size_t ws_bytes,
+                      moe_stream_t stream) {
+  DenseRange range("moe_linear");
+  moe_linear_config c;
+  moe_status st = validate_linear(cfg, &c);
+  if (st != MOE_OK) return st;
+  const LinearLayout L = linear_layout(c, false);
+  if ((st = check_dense_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if (c.M == 0) return MOE_OK;
+  if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
+  const int es = (int)dense_elem(c.dtype);
+  const Span sx{x, c.M, c.K, c.ld_x, es}, sw{w, c.N, c.K, c.ld_w, es}, sb{bias, 1, c.N, c.N, es},
+      sr{residual, c.M, c.N, c.ld_r, es}, sy{y, c.M, c.N, c.ld_y, es}, sz{z, c.M, c.N, c.N, es};
+  const bool in_place = residual == y && c.ld_r == c.ld_y;
+  if ((st = check_spans({sx, sw, sb, in_place ? Span{} : sr}, {sy, sz})) != MOE_OK) return st;
+  DenseGemm g{};
+  g.epi = kDenseLinear;
+  g.act = c.act;
+  g.dtype = c.dtype;
+  g.M = c.M;
+  g.N = c.N;
+  g.K = c.K;
+  g.a = {x, c.ld_x, 1};
+  g.b = {w, c.ld_w, 1};
+  g.bias = bias;
+  g.residual = residual;
+  g.ld_r = c.ld_r;
+  g.out = y;
+  g.ld_o = c.ld_y;
+  g.pre = z;
+  return dense_status(run_product(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, const void *w, const void *z,
+                               const void *dy, void *dx, void *dw, void *dbias, void *ws, size_t ws_bytes,
+                               moe_stream_t stream) {
+  DenseRange range("moe_linear_backward");
+  moe_linear_config c;
+  moe_status st = validate_linear(cfg, &c);
+  if (st != MOE_OK) return st;
+  const LinearLayout L = linear_layout(c, true);
+  if ((st = check_dense_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  const bool act = c.act != MOE_DENSE_IDENTITY;
+  if (!dx && !dw && !dbias) return MOE_ERR_INVALID_ARG;
+  if (c.M > 0 && (!dy || (dw && !x) || (dx && !w) || (act && !z))) return MOE_ERR_INVALID_ARG;
+  const int es = (int)dense_elem(c.dtype);
+  const Span sx{x, c.M, c.K, c.ld_x, es}, sw{w, c.N, c.K, c.ld_w, es},
+      sz{act ? z : nullptr, c.M, c.N, c.N, es}, sdy{dy, c.M, c.N, c.ld_y, es};
+  if ((st = check_spans({sx, sw, sz, sdy}, {Span{dx, c.M, c.K, c.ld_x, es}, Span{dw, c.N, c.K, c.K, es},
+                                            Span{dbias, 1, c.N, c.N, es}})) != MOE_OK)
+    return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *base = static_cast<char *>(ws);
+  cudaError_t e = cudaSuccess;
+  Operand dz{dy, c.ld_y, 1};
+  if (act) {
+    e = launch_act_grad(c.act, c.dtype, c.M, c.N, z, dy, c.ld_y, base + L.dz, s);
+    dz = {base + L.dz, c.N, 1};
+  }
+  DenseGemm g{};
+  g.epi = kDenseStore;
+  g.dtype = c.dtype;
+  if (e == cudaSuccess && dx && c.M > 0) {
+    g.M = c.M;
+    g.N = c.K;
+    g.K = c.N;
+    g.a = dz;
+    g.b = {w, 1, c.ld_w};                   // W [N, K] contracted over its rows
+    g.out = dx;
+    g.ld_o = c.ld_x;
+    e = run_product(g, s);
+  }
+  if (e == cudaSuccess && dw) {
+    g.M = c.N;
+    g.N = c.K;
+    g.K = c.M;
+    g.a = {dz.p, 1, dz.rs};                 // both operands contracted over the rows
+    g.b = {x, 1, c.ld_x};
+    g.out = dw;
+    g.ld_o = c.K;
+    e = run_product(g, s);
+  }
+  if (e == cudaSuccess && dbias)
+    e = launch_colsum(c.dtype, c.M, c.N, dz.p, dz.rs, reinterpret_cast<float *>(base + L.part), dbias, s);
+  return dense_status(e);
+}
+
+moe_status moe_query_gated_ffn_size(const moe_gated_ffn_config *cfg, int32_t backward, size_t *bytes) {
+  moe_gated_ffn_config c;
+  if (!bytes || (backward != 0 && backward != 1)) return MOE_ERR_INVALID_ARG;
+  const moe_status st = validate_gated(cfg, &c);
+  if (st == MOE_OK) *bytes = gated_layout(c, backward != 0).total;
+  return st;
+}
+
+moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const void *w1, const void *b1,
+                         const void *w3, const void *b3, const void *w2, const void *b2,
+                         const void *residual, void *y, void *a, void *u, void *ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+  DenseRange range("moe_gated_ffn");
+  moe_gated_ffn_config c;
+  moe_status st = validate_gated(cfg, &c);
+  if (st != MOE_OK) return st;
+  const GatedLayout L = gated_layout(c, false);
+  if ((st = check_dense_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if (c.T == 0) return MOE_OK;
+  if (!x || !w1 || !w3 || !w2 || !y || !b1 != !b3 || !a != !u) return MOE_ERR_INVALID_ARG;
+  const int es = (int)dense_elem(c.dtype);
+  const int64_t T = c.T, d = c.d_model, f = c.d_ff;
+  const bool in_place = residual == y && c.ld_r == c.ld_y;
+  const Span sr{residual, T, d, c.ld_r, es};
+  if ((st = check_spans({Span{x, T, d, c.ld_x, es}, Span{w1, f, d, d, es}, Span{w3, f, d, d, es},
+                         Span{w2, d, f, f, es}, Span{b1, 1, f, f, es}, Span{b3, 1, f, f, es},
+                         Span{b2, 1, d, d, es}, in_place ? Span{} : sr},
+                        {Span{y, T, d, c.ld_y, es}, Span{a, T, f, f, es}, Span{u, T, f, f, es}})) != MOE_OK)
+    return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *base = static_cast<char *>(ws);
+  DenseGemm g{};
+  g.epi = kDenseGated;
+  g.act = c.act;
+  g.dtype = c.dtype;
+  g.M = T;
+  g.N = c.d_ff;
+  g.K = d;
+  g.a = {x, c.ld_x, 1};
+  g.b = {w1, d, 1};
+  g.b3 = {w3, d, 1};
+  g.bias = b1;
+  g.bias3 = b3;
+  g.out = base + L.h;
+  g.ld_o = f;
+  g.pre = a;
+  g.pre3 = u;
+  cudaError_t e = run_product(g, s);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  DenseGemm q{};
+  q.epi = kDenseLinear;
+  q.act = MOE_DENSE_IDENTITY;
+  q.dtype = c.dtype;
+  q.M = T;
+  q.N = c.d_model;
+  q.K = f;
+  q.a = {base + L.h, f, 1};
+  q.b = {w2, f, 1};
+  q.bias = b2;
+  q.residual = residual;
+  q.ld_r = c.ld_r;
+  q.out = y;
+  q.ld_o = c.ld_y;
+  return dense_status(run_product(q, s));
+}
+
+moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x, const void *w1,
+                                  const void *w3, const void *w2, const void *a, const void *u,
+                                  const void *dy, void *dx, void *dw1, void *db1, void *dw3, void *db3,
+                                  void *dw2, void *db2, void *ws, size_t ws_bytes, moe_stream_t stream) {
+  DenseRange range("moe_gated_ffn_backward");
+  moe_gated_ffn_config c;
+  moe_status st = validate_gated(cfg, &c);
+  if (st != MOE_OK) return st;
+  const GatedLayout L = gated_layout(c, true);
+  if ((st = check_dense_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if (!dw1 != !dw3 || !db1 != !db3 || (!dx && !dw1 && !db1 && !dw2 && !db2)) return MOE_ERR_INVALID_ARG;
+  const bool hidden = dx || dw1 || db1 || dw2;       // dA, dU or h are needed
+  if (c.T > 0 && (!dy || (hidden && (!w2 || !a || !u)) || (dw1 && !x) || (dx && (!w1 || !w3))))
+    return MOE_ERR_INVALID_ARG;
+  const int es = (int)dense_elem(c.dtype);
+  const int64_t T = c.T, d = c.d_model, f = c.d_ff;
+  if ((st = check_spans({Span{x, T, d, c.ld_x, es}, Span{w1, f, d, d, es}, Span{w3, f, d, d, es},
+                         Span{w2, d, f, f, es}, Span{a, T, f, f, es}, Span{u, T, f, f, es},
+                         Span{dy, T, d, c.ld_y, es}},
+                        {Span{dx, T, d, c.ld_x, es}, Span{dw1, f, d, d, es}, Span{db1, 1, f, f, es},
+                         Span{dw3, f, d, d, es}, Span{db3, 1, f, f, es}, Span{dw2, d, f, f, es},
+                         Span{db2, 1, d, d, es}})) != MOE_OK)
+    return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  char *base = static_cast<char *>(ws);
+  char *h = base + L.h, *da = base + L.da, *du = base + L.du;
+  float *part = reinterpret_cast<float *>(base + L.part);
+  cudaError_t e = cudaSuccess;
+  if (hidden && T > 0) {
+    DenseGemm g{};
+    g.epi = kDenseGatedGrad;
+    g.act = c.act;
+    g.dtype = c.dtype;
+    g.M = T;
+    g.N = c.d_ff;
+    g.K = d;
+    g.a = {dy, c.ld_y, 1};
+    g.b = {w2, 1, f};                       // W2 [d, f] contracted over its rows
+    g.pre_in = a;
+    g.pre3_in = u;
+    g.out = da;
+    g.ld_o = f;
+    g.out2 = du;
+    g.out3 = h;
+    e = run_product(g, s);
+  }
+  DenseGemm g{};
+  g.epi = kDenseStore;
+  g.dtype = c.dtype;
+  if (e == cudaSuccess && dx && T > 0) {
+    DenseGemm q = g;
+    q.M = T;
+    q.N = c.d_model;
+    q.K = f;
+    q.a = {da, f, 1};
+    q.b = {w1, 1, d};
+    q.a2 = {du, f, 1};
+    q.b2 = {w3, 1, d};
+    q.out = dx;
+    q.ld_o = c.ld_x;
+    e = run_product(q, s);
+  }
+  g.K = T;
+  // weight gradients [M, N] = left^T right, contracted over the rows
+  auto wgrad = [&](const void *l, int64_t ld_l, int64_t M, const void *r, int64_t ld_r, int32_t N, void *out) {
+    if (e != cudaSuccess || !out) return;
+    g.M = M;
+    g.N = N;
+    g.a = {l, 1, ld_l};
+    g.b = {r, 1, ld_r};
+    g.out = out;
+    g.ld_o = N;
+    e = run_product(g, s);
+  };
+  wgrad(da, f, f, x, c.ld_x, c.d_model, dw1);
+  wgrad(du, f, f, x, c.ld_x, c.d_model, dw3);
+  wgrad(dy, c.ld_y, d, h, f, c.d_ff, dw2);
+  auto bgrad = [&](const void *src, int64_t ld, int32_t N, void *out) {
+    if (e == cudaSuccess && out) e = launch_colsum(c.dtype, T, N, src, ld, part, out, s);
+  };
+  bgrad(da, f, c.d_ff, db1);
+  bgrad(du, f, c.d_ff, db3);
+  bgrad(dy, c.ld_y, c.d_model, db2);
+  return dense_status(e);
+}
+
+static moe_status validate_grads(const moe_grad *g, int32_t count, bool clip) {
+  if (count < 0 || (count > 0 && !g)) return MOE_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].n < 0 || g[i].reserved != 0 || (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16))
+      return MOE_ERR_INVALID_ARG;
+    const int es = (int)dense_elem(g[i].dtype);
+    if (g[i].n > 0 && (!g[i].src || !aligned_to(g[i].src, es) ||
+                       (clip && (!g[i].dst || !aligned_to(g[i].dst, es)))))
+      return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+// In address order, what is written (dst and the norm) may not reach into the next piece.
+static bool grads_overlap(const moe_grad *g, int32_t count, const float *norm) {
+  struct Part {
+    uintptr_t b, e;
+    bool write;
+  };
+  std::vector<Part> v;
+  v.reserve(2 * (size_t)count + 1);
+  const uintptr_t nb = reinterpret_cast<uintptr_t>(norm);
+  if (norm) v.push_back({nb, nb + 4, true});
+  for (int32_t i = 0; i < count; ++i) {
+    if (g[i].n == 0) continue;
+    const uintptr_t n = (uintptr_t)g[i].n * dense_elem(g[i].dtype);
+    const uintptr_t s = reinterpret_cast<uintptr_t>(g[i].src), d = reinterpret_cast<uintptr_t>(g[i].dst);
+    v.push_back({d, d + n, true});
+    if (s != d) v.push_back({s, s + n, false});
+  }
+  std::sort(v.begin(), v.end(), [](const Part &a, const Part &b) { return a.b < b.b; });
+  uintptr_t end_any = 0, end_write = 0;
+  for (const Part &p : v) {
+    if (p.b < end_write || (p.write && p.b < end_any)) return true;
+    end_any = std::max(end_any, p.e);
+    if (p.write) end_write = std::max(end_write, p.e);
+  }
+  return false;
+}
+
+moe_status moe_query_clip_size(int32_t count, size_t *bytes) {
+  if (!bytes || count < 0) return MOE_ERR_INVALID_ARG;
+  Taker t;
+  t.take(clip_scratch(count));
+  *bytes = t.o;
+  return MOE_OK;
+}
+
+static moe_status run_clip(const moe_grad *g, int32_t count, float max_norm, float *norm, void *ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  Taker t;
+  const size_t at = t.take(clip_scratch(count));
+  const moe_status st = check_dense_ws(ws, ws_bytes, t.o);
+  if (st != MOE_OK) return st;
+  return dense_status(launch_clip(g, count, max_norm, norm,
+                                  reinterpret_cast<double *>(static_cast<char *>(ws) + at),
+                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_grad_norm(const moe_grad *grads, int32_t count, float *norm, void *ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+  DenseRange range("moe_grad_norm");
+  const moe_status st = validate_grads(grads, count, false);
+  if (st != MOE_OK) return st;
+  if (!norm || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+  return run_clip(grads, count, -1.0f, norm, ws, ws_bytes, stream);
+}
+
+moe_status moe_clip_grads(const moe_grad *grads, int32_t count, float max_norm, float *norm, void *ws,
+                          size_t ws_bytes, moe_stream_t stream) {
+  DenseRange range("moe_clip_grads");
+  const moe_status st = validate_grads(grads, count, true);
+  if (st != MOE_OK) return st;
+  if (!(max_norm > 0.0f) || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+  try {                                  // (the sort's scratch is host memory)
+    if (grads_overlap(grads, count, norm)) return MOE_ERR_INVALID_ARG;
+  } catch (...) {
+    return MOE_ERR_UNSUPPORTED;
+  }
+  return run_clip(grads, count, max_norm, norm, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,65 @@
+// Host-side declarations of the dense operators beside the MoE layer: the
+// matrix product with bias, activation and residual in its epilogue, the
+// gated feed-forward block, their backward passes, and gradient clipping.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+// A matrix operand of a product: element (row, k) at p + row * rs + k * ks
+// (strides in elements).  ks == 1: the contraction index is contiguous
+// (K-major); rs == 1: the rows are (MN-major).
+struct Operand {
+  const void *p;
+  int64_t rs, ks;
+};
+
+enum DenseEpilogue : int {
+  kDenseStore = 0,      // out = acc
+  kDenseLinear = 1,     // z = acc + bias;  out = act(z) + residual;  pre = z
+  kDenseGated = 2,      // a = acc + bias, u = acc3 + bias3;  out = act(a) * u;  pre = a, pre3 = u
+  kDenseGatedGrad = 3,  // dh = acc, a = pre_in, u = pre3_in:  out = dh u act'(a),
+                        //   out2 = dh act(a),  out3 = act(a) u
+};
+
+// One product  acc[m, n] = sum_k A(m, k) B(n, k)  (+ a second pair of
+// operands a2, b2 contracted over as many k into the same sums) with its
+// epilogue.  kDenseGated contracts A with b into acc and with b3 into acc3.
+// Every matrix of a product has the type `dtype`.
+struct DenseGemm {
+  int epi, act, dtype;
+  int64_t M, K;
+  int32_t N;
+  Operand a, b, b3, a2, b2;      // b3.p / a2.p null: absent
+  const void *bias, *bias3;      // [N] or null
+  const void *residual;          // [M] rows, ld_r apart, or null
+  int64_t ld_r;
+  void *out;                     // [M] rows, ld_o apart
+  int64_t ld_o;
+  void *pre, *pre3;              // [M, N] packed, or null
+  const void *pre_in, *pre3_in;  // [M, N] packed
+  void *out2, *out3;             // [M, N] packed
+};
+
+inline size_t dense_elem(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+// CUDA-core product (dense_simt.cu): any strides, any sizes
+cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
+
+// dz[m, n] = dy[m, n] * act'(z[m, n]); z and dz packed [M, N]
+cudaError_t launch_act_grad(int act, int dtype, int64_t M, int N, const void *z, const void *dy,
+                            int64_t ld_dy, void *dz, cudaStream_t s);
+// out[n] = sum_m src[m, n] in fp32, rows in a fixed order; part: scratch of
+// colsum_scratch(M, N) bytes
+size_t colsum_scratch(int64_t M, int N);
+cudaError_t launch_colsum(int dtype, int64_t M, int N, const void *src, int64_t ld, float *part,
+                          void *out, cudaStream_t s);
+
+// --- gradient clipping (clip.cu) ----------------------------------------------
+size_t clip_scratch(int32_t count);
+// max_norm < 0: the norm alone
+cudaError_t launch_clip(const moe_grad *g, int32_t count, float max_norm, float *norm, double *part,
+                        cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,74 @@
+// Element functions of the dense operators: activations, their derivatives,
+// and loads / stores of one element in fp32.
+#pragma once
+
+#include "device_common.cuh"
+#include "../../include/moe.h"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f32(float &d, float v) { d = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
+
+// 1 / (1 + e^-v).  FAST (bf16 layers, whose results are rounded to 8 bits
+// next): the reciprocal-based division and exponential, a few fp32 ulp.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid_t(float v) {
+  return FAST ? __fdividef(1.0f, 1.0f + __expf(-v)) : 1.0f / (1.0f + expf(-v));
+}
+
+// tanh-form GELU: 0.5 (1 + tanh(y)) = sigmoid(2 y), y = sqrt(2/pi) (v + 0.044715 v^3)
+constexpr float kGeluA = 0.7978845608028654f;       // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+// act(v).  A NaN stays a NaN (relu compares instead of taking a maximum).
+template <bool FAST>
+__device__ __forceinline__ float act_fwd(float v, int act) {
+  switch (act) {
+    case MOE_DENSE_RELU: return v < 0.0f ? 0.0f : v;
+    case MOE_DENSE_SILU: return FAST ? __fdividef(v, 1.0f + __expf(-v)) : v / (1.0f + expf(-v));
+    case MOE_DENSE_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case MOE_DENSE_GELU_TANH:
+      return v * sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
+    default: return v;
+  }
+}
+
+// act(v) and act'(v); relu'(0) = 0, as in the MoE layer's backward pass
+template <bool FAST>
+__device__ __forceinline__ void act_both(float v, int act, float &f, float &d) {
+  switch (act) {
+    case MOE_DENSE_RELU:
+      f = v < 0.0f ? 0.0f : v;
+      d = v > 0.0f ? 1.0f : 0.0f;
+      break;
+    case MOE_DENSE_SILU: {
+      const float s = sigmoid_t<FAST>(v);
+      f = v * s;
+      d = s * (1.0f + v * (1.0f - s));
+      break;
+    }
+    case MOE_DENSE_GELU: {
+      const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));      // normal CDF
+      const float p = 0.3989422804014327f * (FAST ? __expf(-0.5f * v * v) : expf(-0.5f * v * v));
+      f = v * c;
+      d = c + v * p;
+      break;
+    }
+    case MOE_DENSE_GELU_TANH: {
+      const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
+      f = v * s;
+      d = s + v * s * (1.0f - s) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * v * v);
+      break;
+    }
+    default:
+      f = v;
+      d = 1.0f;
+  }
+}
+
+}  // namespace
+}  // namespace moe
