@@ -116,7 +116,16 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
   return L;
 }
 
-cudaError_t run_product(const DenseGemm &g, cudaStream_t s) { return launch_dense_simt(g, s); }
+// n products of one kind: on the tensor cores where all of them fit there
+cudaError_t run_products(const DenseGemm *g, int n, char *ws, cudaStream_t s) {
+  bool tc = true;
+  for (int i = 0; i < n; ++i) tc = tc && dense_tc_ok(g[i]);
+  if (tc) return launch_dense_tc(g, n, reinterpret_cast<uint32_t *>(ws), s);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_dense_simt(g[i], s);
+  return e;
+}
+cudaError_t run_product(const DenseGemm &g, char *ws, cudaStream_t s) { return run_products(&g, 1, ws, s); }
 
 // ---- gated block ------------------------------------------------------------------
 moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *c) {
@@ -198,7 +207,7 @@ moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *w
   g.out = y;
   g.ld_o = c.ld_y;
   g.pre = z;
-  return dense_status(run_product(g, reinterpret_cast<cudaStream_t>(stream)));
+  return dense_status(run_product(g, static_cast<char *>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, const void *w, const void *z,
@@ -238,7 +247,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
     g.b = {w, 1, c.ld_w};                   // W [N, K] contracted over its rows
     g.out = dx;
     g.ld_o = c.ld_x;
-    e = run_product(g, s);
+    e = run_product(g, base, s);
   }
   if (e == cudaSuccess && dw) {
     g.M = c.N;
@@ -248,7 +257,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
     g.b = {x, 1, c.ld_x};
     g.out = dw;
     g.ld_o = c.K;
-    e = run_product(g, s);
+    e = run_product(g, base, s);
   }
   if (e == cudaSuccess && dbias)
     e = launch_colsum(c.dtype, c.M, c.N, dz.p, dz.rs, reinterpret_cast<float *>(base + L.part), dbias, s);
@@ -302,7 +311,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   g.ld_o = f;
   g.pre = a;
   g.pre3 = u;
-  cudaError_t e = run_product(g, s);
+  cudaError_t e = run_product(g, base, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm q{};
   q.epi = kDenseLinear;
@@ -318,7 +327,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   q.ld_r = c.ld_r;
   q.out = y;
   q.ld_o = c.ld_y;
-  return dense_status(run_product(q, s));
+  return dense_status(run_product(q, base, s));
 }
 
 moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x, const void *w1,
@@ -365,7 +374,7 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
     g.ld_o = f;
     g.out2 = du;
     g.out3 = h;
-    e = run_product(g, s);
+    e = run_product(g, base, s);
   }
   DenseGemm g{};
   g.epi = kDenseStore;
@@ -381,23 +390,26 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
     q.b2 = {w3, 1, d};
     q.out = dx;
     q.ld_o = c.ld_x;
-    e = run_product(q, s);
+    e = run_product(q, base, s);
   }
+  // weight gradients [M, N] = left^T right, contracted over the rows: one launch
   g.K = T;
-  // weight gradients [M, N] = left^T right, contracted over the rows
+  DenseGemm wg[3];
+  int nw = 0;
   auto wgrad = [&](const void *l, int64_t ld_l, int64_t M, const void *r, int64_t ld_r, int32_t N, void *out) {
-    if (e != cudaSuccess || !out) return;
+    if (!out) return;
     g.M = M;
     g.N = N;
     g.a = {l, 1, ld_l};
     g.b = {r, 1, ld_r};
     g.out = out;
     g.ld_o = N;
-    e = run_product(g, s);
+    wg[nw++] = g;
   };
   wgrad(da, f, f, x, c.ld_x, c.d_model, dw1);
   wgrad(du, f, f, x, c.ld_x, c.d_model, dw3);
   wgrad(dy, c.ld_y, d, h, f, c.d_ff, dw2);
+  if (e == cudaSuccess && nw > 0) e = run_products(wg, nw, base, s);
   auto bgrad = [&](const void *src, int64_t ld, int32_t N, void *out) {
     if (e == cudaSuccess && out) e = launch_colsum(c.dtype, T, N, src, ld, part, out, s);
   };

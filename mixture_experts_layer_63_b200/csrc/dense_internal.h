@@ -47,6 +47,12 @@ inline size_t dense_elem(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 // CUDA-core product (dense_simt.cu): any strides, any sizes
 cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 
+// Tensor-core products (dense_tc.cu).  dense_tc_ok: bf16 operands whose base
+// and lines are 16-byte aligned.  launch_dense_tc runs up to three products of
+// one kind (same epilogue, same operand orders) in one launch.
+bool dense_tc_ok(const DenseGemm &g);
+cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
+
 // dz[m, n] = dy[m, n] * act'(z[m, n]); z and dz packed [M, N]
 cudaError_t launch_act_grad(int act, int dtype, int64_t M, int N, const void *z, const void *dy,
                             int64_t ld_dy, void *dz, cudaStream_t s);

@@ -1,0 +1,575 @@
+// The dense operators' products on the 5th-generation tensor cores (sm_100a).
+//
+//   acc[m, n] = sum_k A(m, k) B(n, k),  fp32 accumulators in TMEM
+//
+// One persistent CTA pair per two SMs, tiles of 256 rows x bn columns (bn 256
+// or 128).  Per 64-wide k-block each CTA of the pair stages 128 rows of A and
+// half of the B tile by TMA (128-byte swizzle) into a six-stage ring, and the
+// even CTA issues tcgen05.mma.cta_group::2, which reads both CTAs' shared
+// memory: 32 KB a CTA and k-block instead of the 48 KB that a 128 x 256 tile
+// of one CTA takes, whose shared-memory traffic would bound it.  Either operand may be
+// K-major or MN-major in memory (x W^T; dz W; dz^T x), so no transposed copy
+// is ever made.  The accumulators are double-buffered: the epilogue of a tile
+// runs beside the products of the next.
+//
+//   warp 0     TMA producer             warp 2     TMEM allocation
+//   warp 1     MMA issuer (even CTA)    warps 4-7  epilogue, a TMEM lane
+//                                                  (= row of the tile) a thread
+//
+// A product may run over several segments of k (dx = dA W1 + dU W3) and a
+// launch over up to three products (the weight gradients), so that their last
+// waves share the GPU.  Every wait is bounded; on expiry the kernel sets the
+// timeout bit of the workspace's error word, lets its copies and MMAs in
+// flight finish (bounded) and returns.
+#include <algorithm>
+#include <atomic>
+
+#include "dense_internal.h"
+#include "dense_math.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BM = 128;                 // rows of a CTA's half tile
+constexpr int BK = 64;
+constexpr int kStages = 6;
+constexpr int kThreads = 256;
+constexpr int kAccCols = 256;
+constexpr int kTmemCols = 512;
+constexpr uint32_t kABytes = BM * BK * 2;
+constexpr int kStagePerWarp = 32 * 128;      // epilogue staging: 32 rows of 32 fp32
+constexpr int kGroupM = 8;                   // row tiles of a raster group
+constexpr int kMaxProblems = 3;
+constexpr int kMaxSegs = 12;
+
+// A stretch of k-blocks: tensor map and plane (third coordinate) of each operand
+struct Seg {
+  uint8_t a, az, b, bz;
+};
+
+struct TcProblem {
+  CUtensorMap a[2], b[2];
+  int64_t M;
+  int32_t N, KB;                 // k-blocks of one segment
+  int32_t tiles_m, tile_end;     // row tiles; tiles of this and the problems before it
+  const void *bias, *bias3, *residual, *pre_in, *pre3_in;
+  void *out, *pre, *pre3, *out2, *out3;
+  int64_t ld_r, ld_o;
+};
+
+struct TcParams {
+  TcProblem pr[kMaxProblems];
+  Seg seg[kMaxSegs];
+  int32_t segs, nprob, act;
+  int32_t bn, bnh;               // accumulator columns; output columns of a tile
+  uint32_t *err;
+};
+
+struct TilePos {
+  int p, m, n;
+};
+
+// Raster order: groups of kGroupM row tiles, columns outer within a group, so
+// that the pairs at work share few row and column panels in L2.
+__device__ __forceinline__ TilePos tile_pos(const TcParams &P, int t) {
+  TilePos r;
+  r.p = 0;
+  int first = 0;
+  while (r.p + 1 < P.nprob && t >= P.pr[r.p].tile_end) first = P.pr[r.p++].tile_end;
+  t -= first;
+  const int tm = P.pr[r.p].tiles_m, tn = (P.pr[r.p].tile_end - first) / tm;
+  const int g = t / (kGroupM * tn), in = t - g * kGroupM * tn;
+  const int gm = min(kGroupM, tm - g * kGroupM);
+  r.m = g * kGroupM + in % gm;
+  r.n = in / gm;
+  return r;
+}
+
+// ------------------------------- epilogue pieces --------------------------------
+// 32 columns of a thread's row go through the warp's staging buffer: 16-byte
+// piece c of row r at slot c ^ f(r), free of bank conflicts both ways.
+template <typename T>
+__device__ __forceinline__ int stg_at(int r, int c) {
+  constexpr int PIECES = 32 * sizeof(T) / 16;
+  return r * PIECES + (PIECES == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float *v) {
+  if (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4 &w, float *v) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      v[i] = __uint_as_float(q[i]);
+    } else {
+      v[2 * i] = bf16_lo(q[i]);
+      v[2 * i + 1] = bf16_hi(q[i]);
+    }
+  }
+}
+
+// A [M, N] matrix the epilogue reads or writes; vec: its rows are 16-byte
+// aligned, so whole pieces move at once
+template <typename T>
+struct Rows {
+  T *p;
+  int64_t ld, M;
+  int N;
+  bool vec;
+  __device__ Rows(const void *q, int64_t ld_, int64_t M_, int N_)
+      : p(static_cast<T *>(const_cast<void *>(q))), ld(ld_), M(M_), N(N_),
+        vec(((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld_ * (int64_t)sizeof(T))) & 15) == 0) {}
+};
+
+// v[i] of row (row0 + lane) -> column col + i
+template <typename T>
+__device__ __forceinline__ void store32(const Rows<T> &o, int64_t row0, int col, const float (&v)[32],
+                                        uint8_t *stg, int lane) {
+  constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
+  uint4 *s = reinterpret_cast<uint4 *>(stg);
+#pragma unroll
+  for (int c = 0; c < PIECES; ++c) s[stg_at<T>(lane, c)] = pack16<T>(v + c * E);
+  __syncwarp();
+  if (o.vec && col + 32 <= o.N) {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int r = i * (32 / PIECES) + lane / PIECES, c = lane % PIECES;
+      if (row0 + r < o.M) *reinterpret_cast<uint4 *>(o.p + (row0 + r) * o.ld + col + c * E) = s[stg_at<T>(r, c)];
+    }
+  } else if (col < o.N) {
+    const T *e = reinterpret_cast<const T *>(stg);
+    const int rows = (int)min((int64_t)32, o.M - row0);
+    for (int r = 0; r < rows; ++r)
+      if (col + lane < o.N) o.p[(row0 + r) * o.ld + col + lane] = e[stg_at<T>(r, lane / E) * E + lane % E];
+  }
+  __syncwarp();
+}
+
+// the reverse: zeros beyond the matrix
+template <typename T>
+__device__ __forceinline__ void load32(const Rows<T> &o, int64_t row0, int col, float (&v)[32], uint8_t *stg,
+                                       int lane) {
+  constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
+  if (o.vec && col + 32 <= o.N) {
+    const bool in = row0 + lane < o.M;
+    const uint4 *p = reinterpret_cast<const uint4 *>(o.p + (row0 + lane) * o.ld + col);
+    uint4 w[PIECES];
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) w[c] = in ? p[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) unpack16<T>(w[c], v + c * E);
+    return;
+  }
+  T *e = reinterpret_cast<T *>(stg);
+  const int rows = (int)max((int64_t)0, min((int64_t)32, o.M - row0));
+  T zero;
+  from_f32(zero, 0.0f);
+  for (int r = 0; r < 32; ++r)
+    e[stg_at<T>(r, lane / E) * E + lane % E] =
+        r < rows && col + lane < o.N ? o.p[(row0 + r) * o.ld + col + lane] : zero;
+  __syncwarp();
+  const uint4 *s = reinterpret_cast<const uint4 *>(stg);
+#pragma unroll
+  for (int c = 0; c < PIECES; ++c) unpack16<T>(s[stg_at<T>(lane, c)], v + c * E);
+  __syncwarp();
+}
+
+__device__ __forceinline__ void acc32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld32(taddr, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void add_bias(float (&v)[32], const float *bias) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(bias + i);
+    v[i] += b.x;
+    v[i + 1] += b.y;
+    v[i + 2] += b.z;
+    v[i + 3] += b.w;
+  }
+}
+
+// This warp's 32 rows (row0 ...) x the tile's output columns (col0 ...) from
+// the accumulator at taddr.  sb: the tile's bias columns in shared memory.
+template <int EPI, typename T>
+__device__ __forceinline__ void epilogue(const TcParams &P, const TcProblem &Q, uint32_t taddr, int64_t row0,
+                                         int col0, const float *sb, uint8_t *stg, int lane) {
+  constexpr bool FAST = sizeof(T) == 2;
+  const Rows<T> out(Q.out, Q.ld_o, Q.M, Q.N);
+  if (row0 >= Q.M) return;
+  for (int c = 0; c < P.bnh && col0 + c < Q.N; c += 32) {
+    float v[32];
+    acc32(taddr + c, v);
+    const int col = col0 + c;
+    if (EPI == kDenseStore) {
+      store32(out, row0, col, v, stg, lane);
+    } else if (EPI == kDenseLinear) {
+      if (Q.bias) add_bias(v, sb + c);
+      if (Q.pre) store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
+      if (P.act != MOE_DENSE_IDENTITY) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act);
+      }
+      if (Q.residual) {
+        float r[32];
+        load32(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col, r, stg, lane);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += r[i];
+      }
+      store32(out, row0, col, v, stg, lane);
+    } else if (EPI == kDenseGated) {
+      float u[32];
+      acc32(taddr + P.bnh + c, u);
+      if (Q.bias) {
+        add_bias(v, sb + c);
+        add_bias(u, sb + P.bnh + c);
+      }
+      if (Q.pre) {
+        store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
+        store32(Rows<T>(Q.pre3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act) * u[i];
+      store32(out, row0, col, v, stg, lane);
+    } else {                                             // kDenseGatedGrad
+      float a[32], u[32];
+      load32(Rows<T>(Q.pre_in, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
+      load32(Rows<T>(Q.pre3_in, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float f, d;
+        act_both<FAST>(a[i], P.act, f, d);
+        const float dh = v[i];
+        v[i] = dh * u[i] * d;
+        a[i] = dh * f;
+        u[i] = f * u[i];
+      }
+      store32(out, row0, col, v, stg, lane);
+      store32(Rows<T>(Q.out2, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
+      store32(Rows<T>(Q.out3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+    }
+  }
+}
+
+// --------------------------------- the kernel ----------------------------------
+template <int EPI, bool AMN, bool BMN, typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    dense_pair_kernel(const __grid_constant__ TcParams P) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kStages];
+  __shared__ __align__(8) uint64_t empty_bar[kStages];
+  __shared__ __align__(8) uint64_t accf_bar[2];
+  __shared__ __align__(8) uint64_t acce_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(16) float s_bias[4][kAccCols];       // a copy for each epilogue warp
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  __shared__ uint64_t s_limit_sh;
+
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t b_bytes = (uint32_t)(P.bn / 2) * BK * 2;
+  const uint32_t stage_bytes = kABytes + b_bytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int tiles = P.pr[P.nprob - 1].tile_end;
+
+  if (tid == 32) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(&full_bar[st], 1);
+      mbar_init(&empty_bar[st], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&accf_bar[a], 1);
+      mbar_init(&acce_bar[a], 2 * 4 * 32);
+    }
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (tid == 0) {
+    tma_prefetch_map(&P.pr[0].a[0]);
+    tma_prefetch_map(&P.pr[0].b[0]);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) s_limit_sh = wait_limit_ns(P.err);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem_base;
+  const uint64_t s_limit = s_limit_sh;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      const TilePos q = tile_pos(P, t);
+      const TcProblem &Q = P.pr[q.p];
+      const int am = q.m * 2 * BM + (int)rank * BM;
+      // gated: the even CTA stages rows of W1, the odd one the same rows of W3
+      const int bn0 = q.n * P.bnh + (EPI == kDenseGated ? 0 : (int)rank * (P.bn / 2));
+      for (int sg = 0; ok && sg < P.segs; ++sg) {
+        const Seg S = P.seg[sg];
+        const CUtensorMap *ma = &Q.a[S.a];
+        const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
+        for (int kb = 0; kb < Q.KB; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) { ok = false; break; }
+          uint8_t *sa = smem + (size_t)stage * stage_bytes;
+          uint8_t *sb = sa + kABytes;
+          const uint32_t fb = smem_u32(&full_bar[stage]) & 0xFEFFFFFFu;      // the even CTA's barrier
+          if (rank == 0) {
+            mbar_expect_tx(&full_bar[stage], 2 * stage_bytes);
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          }
+          if (AMN) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tma_load_3d_pair(sa + j * 8192, ma, fb, am + j * 64, kb * BK, S.az);
+          } else {
+            tma_load_3d_pair(sa, ma, fb, kb * BK, am, S.az);
+          }
+          // 64-line boxes (8 KB) either way: one or two of them are this CTA's half
+          for (int j = 0; j < P.bn / 128; ++j) {
+            if (BMN) tma_load_3d_pair(sb + j * 8192, mb, fb, bn0 + j * 64, kb * BK, S.bz);
+            else tma_load_3d_pair(sb + j * 8192, mb, fb, kb * BK, bn0 + j * 64, S.bz);
+          }
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
+      }
+    }
+    if (!ok && rank == 0) {
+      for (int st = 0; st < kStages; ++st)
+        if (armed & (1u << st)) mbar_wait_drain(&full_bar[st], (armed_parity >> st) & 1u);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ------------------------ MMA issuer (even CTA only) ------------------------
+    const uint32_t idesc = idesc_bf16(2 * BM, P.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      const int nkb = P.segs * P.pr[tile_pos(P, t).p].KB;
+      if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t a_addr = smem_u32(smem + (size_t)stage * stage_bytes);
+        const uint32_t b_addr = a_addr + kABytes;
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k)
+          umma_bf16_pair(d_tmem, AMN ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
+                         BMN ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc,
+                         (kb > 0 || k > 0) ? 1u : 0u);
+        umma_commit_pair_both(&empty_bar[stage]);
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) break;
+      umma_commit_pair_both(&accf_bar[acc]);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+    umma_commit_pair_local(&drain_bar);
+    mbar_wait_drain(&drain_bar, 0);
+  } else if (warp >= 4) {
+    // -------------------------------- epilogue --------------------------------
+    const int ew = warp - 4;
+    uint8_t *stg = smem + (size_t)kStages * stage_bytes + (size_t)ew * kStagePerWarp;
+    const uint32_t acce_even[2] = {mapa_shared(smem_u32(&acce_bar[0]), 0), mapa_shared(smem_u32(&acce_bar[1]), 0)};
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = pair; t < tiles; t += npairs) {
+      const TilePos q = tile_pos(P, t);
+      const TcProblem &Q = P.pr[q.p];
+      const int col0 = q.n * P.bnh;
+      if ((EPI == kDenseLinear || EPI == kDenseGated) && Q.bias) {
+        for (int i = lane; i < P.bn; i += 32) {
+          const bool up = EPI == kDenseGated && i >= P.bnh;
+          const int n = col0 + (up ? i - P.bnh : i);
+          s_bias[ew][i] = n < Q.N ? to_f32(static_cast<const T *>(up ? Q.bias3 : Q.bias)[n]) : 0.0f;
+        }
+        __syncwarp();
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit))) break;
+      tc_fence_after();
+      epilogue<EPI, T>(P, Q, tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(ew * 32) << 16),
+                       (int64_t)q.m * 2 * BM + rank * BM + ew * 32, col0, s_bias[ew], stg, lane);
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive_cluster(acce_even[acc]);
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_all();              // neither CTA leaves while the pair may still touch it
+  tc_fence_after();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols));
+}
+
+// ------------------------------- host side --------------------------------------
+constexpr int kMaxDevices = 64;
+
+// As many CTA pairs as fit at once.  The attribute is set and the occupancy
+// asked once a device (a second thread that asks meanwhile gets the same).
+template <auto kern>
+cudaError_t pairs_of(size_t smem, int *pairs) {
+  static std::atomic<int> cache[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < kMaxDevices ? cache[dev].load(std::memory_order_acquire) : 0;
+  if (n == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (device_sms() / 2), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = device_sms() / 2;
+    }
+    if (dev < kMaxDevices) cache[dev].store(n, std::memory_order_release);
+  }
+  *pairs = n;
+  return cudaSuccess;
+}
+
+constexpr size_t kSmemBytes = 1024 + kStages * (kABytes + 128 * BK * 2) + 4 * kStagePerWarp;
+
+template <int EPI, bool AMN, bool BMN, typename T>
+cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
+  constexpr auto kern = dense_pair_kernel<EPI, AMN, BMN, T>;
+  int pairs = 0;
+  cudaError_t e = pairs_of<kern>(kSmemBytes, &pairs);
+  if (e != cudaSuccess) return e;
+  // columns of a tile: the width whose last wave wastes less (a 128-column
+  // tile costs about 0.55 of a 256-column one)
+  auto waves = [&](int bn) {
+    int64_t tiles = 0;
+    for (int p = 0; p < P.nprob; ++p) {
+      const int bnh = EPI == kDenseGated ? bn / 2 : bn;
+      tiles += (int64_t)P.pr[p].tiles_m * ((P.pr[p].N + bnh - 1) / bnh);
+    }
+    return (double)((tiles + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55);
+  };
+  P.bn = waves(128) < waves(256) ? 128 : 256;
+  P.bnh = EPI == kDenseGated ? P.bn / 2 : P.bn;
+  int64_t end = 0;
+  for (int p = 0; p < P.nprob; ++p) {
+    end += (int64_t)P.pr[p].tiles_m * ((P.pr[p].N + P.bnh - 1) / P.bnh);
+    if (end > 0x3fffffff) return cudaErrorInvalidValue;
+    P.pr[p].tile_end = (int32_t)end;
+  }
+  return launch_kernel(kern, 2 * (unsigned)std::min<int64_t>(pairs, end), kThreads, kSmemBytes, s, P);
+}
+
+bool kmajor(const Operand &o) { return o.ks == 1; }
+
+// `rows` x K bf16 operand for TMA: 16-byte aligned base and lines
+bool tma_ok(const Operand &o, int64_t rows, int64_t K) {
+  if (!kmajor(o) && o.rs != 1) return false;
+  const int64_t ld = kmajor(o) ? o.rs : o.ks, lines = kmajor(o) ? rows : K;
+  return (reinterpret_cast<uintptr_t>(o.p) & 15) == 0 && (lines == 1 || ld % 8 == 0);
+}
+
+// Map {inner, lines, planes} of an operand in boxes of 64 inner elements x
+// `box` lines x 1 plane, 128-byte swizzle
+bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t K, int box, int planes,
+                 int64_t plane_stride) {
+  const bool km = kmajor(o);
+  const int64_t inner = km ? K : rows, lines = km ? rows : K;
+  const int64_t ld = lines == 1 ? (inner + 7) / 8 * 8 : (km ? o.rs : o.ks);
+  return make_map3d(m, o.p, inner, lines, planes, ld, planes == 1 ? ld * lines : plane_stride, box);
+}
+
+}  // namespace
+
+bool dense_tc_ok(const DenseGemm &g) {
+  if (g.dtype != MOE_BF16 || g.K < 1 || g.M < 1) return false;
+  if (g.M > 0x7ffffe00 || g.K > 0x7ffffe00 || g.N > 0x7ffffe00) return false;
+  for (const Operand *o : {&g.b, &g.b3, &g.b2})
+    if (o->p && !tma_ok(*o, g.N, g.K)) return false;
+  for (const Operand *o : {&g.a, &g.a2})
+    if (o->p && !tma_ok(*o, g.M, g.K)) return false;
+  const bool am = !kmajor(g.a), bm = !kmajor(g.b);
+  if (g.a2.p && (am != !kmajor(g.a2) || bm != !kmajor(g.b2))) return false;
+  if (g.epi == kDenseLinear || g.epi == kDenseGated) return !am && !bm && (!g.b3.p || kmajor(g.b3));
+  if (g.epi == kDenseGatedGrad) return !am && bm;
+  return bm;
+}
+
+cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s) {
+  if (n < 1 || n > kMaxProblems) return cudaErrorInvalidValue;
+  TcParams P{};
+  P.err = err;
+  P.act = g[0].act;
+  P.nprob = n;
+  P.segs = g[0].a2.p ? 2 : 1;
+  for (int i = 0; i < P.segs; ++i) P.seg[i] = {(uint8_t)i, 0, (uint8_t)i, 0};
+  // the boxes' height depends on the tile width, which launch_pair_as picks;
+  // both widths are a multiple of 64, so maps of 64-line boxes serve K-major
+  // B of 128 columns and two loads of them the 256-column tile
+  for (int p = 0; p < n; ++p) {
+    TcProblem &Q = P.pr[p];
+    const DenseGemm &G = g[p];
+    bool ok = map_operand(&Q.a[0], G.a, G.M, G.K, kmajor(G.a) ? BM : BK, 1, 0) &&
+              map_operand(&Q.b[0], G.b, G.N, G.K, BK, 1, 0);
+    if (G.a2.p)
+      ok = ok && map_operand(&Q.a[1], G.a2, G.M, G.K, kmajor(G.a2) ? BM : BK, 1, 0) &&
+           map_operand(&Q.b[1], G.b2, G.N, G.K, BK, 1, 0);
+    if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, BK, 1, 0);
+    if (!ok) return cudaErrorInvalidValue;
+    Q.M = G.M;
+    Q.N = G.N;
+    Q.KB = (int32_t)((G.K + BK - 1) / BK);
+    Q.tiles_m = (int32_t)((G.M + 2 * BM - 1) / (2 * BM));
+    Q.bias = G.bias;
+    Q.bias3 = G.bias3;
+    Q.residual = G.residual;
+    Q.ld_r = G.ld_r;
+    Q.out = G.out;
+    Q.ld_o = G.ld_o;
+    Q.pre = G.pre;
+    Q.pre3 = G.pre3;
+    Q.pre_in = G.pre_in;
+    Q.pre3_in = G.pre3_in;
+    Q.out2 = G.out2;
+    Q.out3 = G.out3;
+  }
+  using B = __nv_bfloat16;
+  switch (g[0].epi) {
+    case kDenseLinear: return launch_pair_as<kDenseLinear, false, false, B>(P, s);
+    case kDenseGated: return launch_pair_as<kDenseGated, false, false, B>(P, s);
+    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, false, true, B>(P, s);
+    default:
+      return kmajor(g[0].a) ? launch_pair_as<kDenseStore, false, true, B>(P, s)
+                            : launch_pair_as<kDenseStore, true, true, B>(P, s);
+  }
+}
+
+}  // namespace moe
