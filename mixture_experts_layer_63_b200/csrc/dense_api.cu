@@ -110,7 +110,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
   Taker t;
   if (backward) {
     L.dz = t.take(c.act != MOE_DENSE_IDENTITY ? (size_t)c.M * c.N * dense_elem(c.dtype) : 0);
-    L.part = t.take(colsum_scratch(c.M, c.N));
+    L.part = t.take(colsum_scratch(c.M, c.N, 1));
   }
   L.total = t.o;
   return L;
@@ -155,7 +155,7 @@ GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
   if (backward) {
     L.da = t.take(tf);
     L.du = t.take(tf);
-    L.part = t.take(colsum_scratch(c.T, std::max(c.d_ff, c.d_model)));
+    L.part = t.take(colsum_scratch(c.T, std::max(c.d_ff, c.d_model), 3));
   }
   L.total = t.o;
   return L;
@@ -232,9 +232,11 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
   char *base = static_cast<char *>(ws);
   cudaError_t e = cudaSuccess;
   Operand dz{dy, c.ld_y, 1};
-  if (act) {
-    e = launch_act_grad(c.act, c.dtype, c.M, c.N, z, dy, c.ld_y, base + L.dz, s);
-    dz = {base + L.dz, c.N, 1};
+  if (act || dbias) {
+    // dz and its column sums in one pass over dy and z
+    const ColSum q{dy, c.ld_y, c.N, act ? z : nullptr, act ? base + L.dz : nullptr, dbias};
+    e = launch_colsums(c.act, c.dtype, c.M, &q, 1, reinterpret_cast<float *>(base + L.part), s);
+    if (act) dz = {base + L.dz, c.N, 1};
   }
   DenseGemm g{};
   g.epi = kDenseStore;
@@ -259,8 +261,6 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
     g.ld_o = c.K;
     e = run_product(g, base, s);
   }
-  if (e == cudaSuccess && dbias)
-    e = launch_colsum(c.dtype, c.M, c.N, dz.p, dz.rs, reinterpret_cast<float *>(base + L.part), dbias, s);
   return dense_status(e);
 }
 
@@ -410,12 +410,12 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   wgrad(du, f, f, x, c.ld_x, c.d_model, dw3);
   wgrad(dy, c.ld_y, d, h, f, c.d_ff, dw2);
   if (e == cudaSuccess && nw > 0) e = run_products(wg, nw, base, s);
-  auto bgrad = [&](const void *src, int64_t ld, int32_t N, void *out) {
-    if (e == cudaSuccess && out) e = launch_colsum(c.dtype, T, N, src, ld, part, out, s);
-  };
-  bgrad(da, f, c.d_ff, db1);
-  bgrad(du, f, c.d_ff, db3);
-  bgrad(dy, c.ld_y, c.d_model, db2);
+  ColSum bq[3];
+  int nb = 0;
+  if (db1) bq[nb++] = {da, f, c.d_ff, nullptr, nullptr, db1};
+  if (db3) bq[nb++] = {du, f, c.d_ff, nullptr, nullptr, db3};
+  if (db2) bq[nb++] = {dy, c.ld_y, c.d_model, nullptr, nullptr, db2};
+  if (e == cudaSuccess && nb > 0) e = launch_colsums(0, c.dtype, T, bq, nb, part, s);
   return dense_status(e);
 }
 

@@ -53,14 +53,21 @@ cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 bool dense_tc_ok(const DenseGemm &g);
 cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
 
-// dz[m, n] = dy[m, n] * act'(z[m, n]); z and dz packed [M, N]
-cudaError_t launch_act_grad(int act, int dtype, int64_t M, int N, const void *z, const void *dy,
-                            int64_t ld_dy, void *dz, cudaStream_t s);
-// out[n] = sum_m src[m, n] in fp32, rows in a fixed order; part: scratch of
-// colsum_scratch(M, N) bytes
-size_t colsum_scratch(int64_t M, int N);
-cudaError_t launch_colsum(int dtype, int64_t M, int N, const void *src, int64_t ld, float *part,
-                          void *out, cudaStream_t s);
+// Column sums out[n] = sum_m src[m, n] (fp32, in a fixed order), up to three
+// matrices of M rows in one launch.  With z and dz (packed [M, N]):
+// dz = src * act'(z) first, and the sums are dz's; out may then be null.
+// part: scratch of colsum_scratch(M, widest N, count) bytes.
+constexpr int kMaxColSums = 3;
+struct ColSum {
+  const void *src;
+  int64_t ld;
+  int N;
+  const void *z;
+  void *dz, *out;
+};
+size_t colsum_scratch(int64_t M, int N, int count);
+cudaError_t launch_colsums(int act, int dtype, int64_t M, const ColSum *q, int count, float *part,
+                           cudaStream_t s);
 
 // --- gradient clipping (clip.cu) ----------------------------------------------
 size_t clip_scratch(int32_t count);

@@ -13,6 +13,29 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float &d, float v) { d = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
 
+// 16 bytes of T from fp32 values, and back
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float *v) {
+  if (sizeof(T) == 4)
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4 &w, float *v) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (sizeof(T) == 4) {
+      v[i] = __uint_as_float(q[i]);
+    } else {
+      v[2 * i] = bf16_lo(q[i]);
+      v[2 * i + 1] = bf16_hi(q[i]);
+    }
+  }
+}
+
 // 1 / (1 + e^-v).  FAST (bf16 layers, whose results are rounded to 8 bits
 // next): the reciprocal-based division and exponential, a few fp32 ulp.
 template <bool FAST>

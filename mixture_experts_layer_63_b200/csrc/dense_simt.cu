@@ -130,60 +130,125 @@ __global__ void __launch_bounds__(256) dense_simt_kernel(const DenseGemm P) {
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) act_grad_kernel(int act, int64_t M, int N, const T *z, const T *dy,
-                                                       int64_t ld_dy, T *dz) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t total = M * N;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t m = i / N;
-    float f, d;
-    act_both<sizeof(T) == 2>(to_f32(z[i]), act, f, d);
-    from_f32(dz[i], to_f32(dy[m * ld_dy + (i - m * N)]) * d);
-  }
-}
+// Column sums, and dz = dy act'(z) on the way (ACT): a warp reads rows of 32
+// pieces of V = 16 / sizeof(T) columns; block (x, y) adds the rows of part y,
+// eight interleaved, and leaves their sums in part[y][n]; the second kernel
+// adds the parts in order.  dz enters its sums before its rounding.  No
+// atomics: the same bits on every call.
+struct ColSums {
+  ColSum q[kMaxColSums];
+  int64_t M;
+  int parts, act;
+  float *part;                 // [count][parts][max N]
+  int64_t part_stride;
+};
 
-// Column sums in two passes without atomics: block (x, y) adds the rows of
-// part y in ascending order, 8 interleaved rows to a block, into part[y][n];
-// the second kernel adds the parts in order.
-constexpr int kColRows = 256;          // rows of a part at least
-constexpr int kColParts = 64;          // parts at most
-
-int colsum_parts(int64_t M) {
-  return (int)std::min<int64_t>(kColParts, std::max<int64_t>(1, (M + kColRows - 1) / kColRows));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) colsum_part_kernel(int64_t M, int N, const T *src, int64_t ld,
-                                                          float *part) {
-  __shared__ float red[8][33];
+template <typename T, bool ACT>
+__global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
+  constexpr int V = 16 / sizeof(T);
+  __shared__ float red[8][32 * V];
+  const ColSum Q = P.q[blockIdx.z];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  const int n = blockIdx.x * 32 + lane;
-  const int64_t per = (M + gridDim.y - 1) / gridDim.y;
-  const int64_t r0 = blockIdx.y * per, r1 = min(M, r0 + per);
+  const int n0 = blockIdx.x * 32 * V;
+  const int64_t per = (P.M + P.parts - 1) / P.parts;
+  const int64_t r0 = blockIdx.y * per, r1 = min(P.M, r0 + per);
   pdl_wait();
   pdl_trigger();
-  float v = 0.0f;
-  if (n < N)
-    for (int64_t r = r0 + w; r < r1; r += 8) v += to_f32(src[r * ld + n]);
-  red[w][lane] = v;
+  if (n0 >= Q.N) return;
+  const T *src = static_cast<const T *>(Q.src), *z = static_cast<const T *>(Q.z);
+  T *dz = static_cast<T *>(Q.dz);
+  float sum[V] = {};
+  uintptr_t at = reinterpret_cast<uintptr_t>(src) | (uintptr_t)(Q.ld * (int64_t)sizeof(T));
+  if (ACT) at |= reinterpret_cast<uintptr_t>(z) | (uintptr_t)((int64_t)Q.N * sizeof(T));
+  const int n = n0 + lane * V;
+  if ((at & 15) == 0 && n0 + 32 * V <= Q.N) {
+    // whole 16-byte pieces, four rows in flight
+    constexpr int R = 4;
+    for (int64_t r = r0 + w; r < r1; r += 8 * R) {
+      uint4 a[R], b[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (r + 8 * i < r1) {
+          a[i] = *reinterpret_cast<const uint4 *>(src + (r + 8 * i) * Q.ld + n);
+          if (ACT) b[i] = *reinterpret_cast<const uint4 *>(z + (r + 8 * i) * Q.N + n);
+        }
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (r + 8 * i >= r1) break;
+        float v[V];
+        unpack16<T>(a[i], v);
+        if (ACT) {
+          float zz[V];
+          unpack16<T>(b[i], zz);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float f, d;
+            act_both<sizeof(T) == 2>(zz[j], P.act, f, d);
+            v[j] *= d;
+          }
+          *reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.N + n) = pack16<T>(v);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] += v[j];
+      }
+    }
+  } else {
+    // column j of a lane is n0 + 32 j + lane
+    for (int64_t r = r0 + w; r < r1; r += 8)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int c = n0 + 32 * j + lane;
+        if (c >= Q.N) break;
+        float v = to_f32(src[r * Q.ld + c]);
+        if (ACT) {
+          float f, d;
+          act_both<sizeof(T) == 2>(to_f32(z[r * Q.N + c]), P.act, f, d);
+          v *= d;
+          from_f32(dz[r * Q.N + c], v);
+        }
+        sum[j] += v;
+      }
+  }
+  if (!Q.out) return;                     // dz alone is wanted
+  const bool pieces = (at & 15) == 0 && n0 + 32 * V <= Q.N;
+#pragma unroll
+  for (int j = 0; j < V; ++j) red[w][pieces ? lane * V + j : 32 * j + lane] = sum[j];
   __syncthreads();
-  if (w == 0 && n < N) {
-    for (int i = 1; i < 8; ++i) v += red[i][lane];
-    part[(int64_t)blockIdx.y * N + n] = v;
+  for (int c = threadIdx.x; c < 32 * V && n0 + c < Q.N; c += 256) {
+    float v = red[0][c];
+    for (int i = 1; i < 8; ++i) v += red[i][c];
+    P.part[(blockIdx.z * (int64_t)P.parts + blockIdx.y) * P.part_stride + n0 + c] = v;
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) colsum_join_kernel(int parts, int N, const float *part, T *out) {
+__global__ void __launch_bounds__(256) colsum_join_kernel(const ColSums P) {
+  const ColSum Q = P.q[blockIdx.z];
   const int n = blockIdx.x * 256 + threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  if (n >= N) return;
+  if (n >= Q.N || !Q.out) return;
+  const float *p = P.part + blockIdx.z * (int64_t)P.parts * P.part_stride + n;
   float v = 0.0f;
-  for (int p = 0; p < parts; ++p) v += part[(int64_t)p * N + n];
-  from_f32(out[n], v);
+#pragma unroll 8
+  for (int i = 0; i < P.parts; ++i) v += p[i * P.part_stride];
+  from_f32(static_cast<T *>(Q.out)[n], v);
+}
+
+// enough row parts for some eight blocks an SM, at least 32 rows each
+int colsum_parts(int64_t M, int N) {
+  const int64_t cols = std::max(1, N / 256);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({64, (M + 31) / 32, (148 * 8 + cols - 1) / cols}));
+}
+
+template <typename T>
+cudaError_t colsums_as(const ColSums &P, int count, int maxN, bool act, bool join, cudaStream_t s) {
+  constexpr int W = 32 * (16 / sizeof(T));
+  const dim3 grid((maxN + W - 1) / W, P.parts, count);
+  const cudaError_t e = act ? launch_kernel(colsum_part_kernel<T, true>, grid, 256, 0, s, P)
+                            : launch_kernel(colsum_part_kernel<T, false>, grid, 256, 0, s, P);
+  if (e != cudaSuccess || !join) return e;
+  return launch_kernel(colsum_join_kernel<T>, dim3((maxN + 255) / 256, 1, count), 256, 0, s, P);
 }
 
 unsigned grid_for(int64_t blocks, int per_sm) {
@@ -204,37 +269,26 @@ cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s) {
                : launch_kernel(dense_simt_kernel<__nv_bfloat16, false>, grid, 256, 0, s, g);
 }
 
-cudaError_t launch_act_grad(int act, int dtype, int64_t M, int N, const void *z, const void *dy,
-                            int64_t ld_dy, void *dz, cudaStream_t s) {
-  if (M == 0) return cudaSuccess;
-  const unsigned grid = grid_for((M * N + 255) / 256, 8);
-  if (dtype == MOE_F32)
-    return launch_kernel(act_grad_kernel<float>, grid, 256, 0, s, act, M, N, static_cast<const float *>(z),
-                         static_cast<const float *>(dy), ld_dy, static_cast<float *>(dz));
-  return launch_kernel(act_grad_kernel<__nv_bfloat16>, grid, 256, 0, s, act, M, N,
-                       static_cast<const __nv_bfloat16 *>(z), static_cast<const __nv_bfloat16 *>(dy), ld_dy,
-                       static_cast<__nv_bfloat16 *>(dz));
-}
+size_t colsum_scratch(int64_t M, int N, int count) { return (size_t)colsum_parts(M, N) * N * 4 * count; }
 
-size_t colsum_scratch(int64_t M, int N) { return (size_t)colsum_parts(M) * N * 4; }
-
-cudaError_t launch_colsum(int dtype, int64_t M, int N, const void *src, int64_t ld, float *part, void *out,
-                          cudaStream_t s) {
-  const int parts = colsum_parts(M);
-  const dim3 grid((N + 31) / 32, parts);
-  const unsigned gj = (N + 255) / 256;
-  cudaError_t e;
-  if (dtype == MOE_F32) {
-    e = launch_kernel(colsum_part_kernel<float>, grid, 256, 0, s, M, N, static_cast<const float *>(src), ld,
-                      part);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(colsum_join_kernel<float>, gj, 256, 0, s, parts, N, part, static_cast<float *>(out));
+cudaError_t launch_colsums(int act, int dtype, int64_t M, const ColSum *q, int count, float *part,
+                           cudaStream_t s) {
+  ColSums P{};
+  int maxN = 0;
+  bool grad = false, join = false;
+  for (int i = 0; i < count; ++i) {
+    P.q[i] = q[i];
+    maxN = std::max(maxN, q[i].N);
+    grad = grad || q[i].dz;
+    join = join || q[i].out;
   }
-  e = launch_kernel(colsum_part_kernel<__nv_bfloat16>, grid, 256, 0, s, M, N,
-                    static_cast<const __nv_bfloat16 *>(src), ld, part);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(colsum_join_kernel<__nv_bfloat16>, gj, 256, 0, s, parts, N, part,
-                       static_cast<__nv_bfloat16 *>(out));
+  P.M = M;
+  P.act = act;
+  P.parts = colsum_parts(M, maxN);
+  P.part = part;
+  P.part_stride = maxN;
+  return dtype == MOE_F32 ? colsums_as<float>(P, count, maxN, grad, join, s)
+                          : colsums_as<__nv_bfloat16>(P, count, maxN, grad, join, s);
 }
 
 }  // namespace moe

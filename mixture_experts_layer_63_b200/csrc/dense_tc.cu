@@ -13,7 +13,7 @@
 // runs beside the products of the next.
 //
 //   warp 0     TMA producer             warp 2     TMEM allocation
-//   warp 1     MMA issuer (even CTA)    warps 4-7  epilogue, a TMEM lane
+//   warp 1     MMA issuer (even CTA)    warps 4-11 epilogue, a TMEM lane
 //                                                  (= row of the tile) a thread
 //
 // A product may run over several segments of k (dx = dA W1 + dU W3) and a
@@ -33,13 +33,20 @@ namespace {
 
 constexpr int BM = 128;                 // rows of a CTA's half tile
 constexpr int BK = 64;
-constexpr int kStages = 6;
-constexpr int kThreads = 256;
+#ifndef DT_BKS
+#define DT_BKS 2
+#endif
+#ifndef DT_GM
+#define DT_GM 16
+#endif
+constexpr int kBks = DT_BKS;                 // k-blocks of a stage
+constexpr int kStages = 6 / kBks;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kABytes = BM * BK * 2;
-constexpr int kStagePerWarp = 32 * 128;      // epilogue staging: 32 rows of 32 fp32
-constexpr int kGroupM = 8;                   // row tiles of a raster group
+constexpr int kGroupM = DT_GM;                   // row tiles of a raster group
 constexpr int kMaxProblems = 3;
 constexpr int kMaxSegs = 12;
 
@@ -95,28 +102,6 @@ __device__ __forceinline__ int stg_at(int r, int c) {
   return r * PIECES + (PIECES == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float *v) {
-  if (sizeof(T) == 4)
-    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack16(const uint4 &w, float *v) {
-  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (sizeof(T) == 4) {
-      v[i] = __uint_as_float(q[i]);
-    } else {
-      v[2 * i] = bf16_lo(q[i]);
-      v[2 * i + 1] = bf16_hi(q[i]);
-    }
-  }
-}
-
 // A [M, N] matrix the epilogue reads or writes; vec: its rows are 16-byte
 // aligned, so whole pieces move at once
 template <typename T>
@@ -154,34 +139,43 @@ __device__ __forceinline__ void store32(const Rows<T> &o, int64_t row0, int col,
   __syncwarp();
 }
 
-// the reverse: zeros beyond the matrix
+// The reverse in two steps: fetch reads the warp's 32 x 32 elements (zeros
+// beyond the matrix) into registers, every load instruction whole 64- or
+// 128-byte row pieces (a thread reading its own row would touch 32 lines an
+// instruction and fetch every sector twice: there is next to no L1 beside
+// the stages); get hands each thread its row through the staging buffer.
 template <typename T>
-__device__ __forceinline__ void load32(const Rows<T> &o, int64_t row0, int col, float (&v)[32], uint8_t *stg,
-                                       int lane) {
-  constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
-  if (o.vec && col + 32 <= o.N) {
-    const bool in = row0 + lane < o.M;
-    const uint4 *p = reinterpret_cast<const uint4 *>(o.p + (row0 + lane) * o.ld + col);
-    uint4 w[PIECES];
+struct Piece32 {
+  static constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
+  uint4 w[PIECES];
+  __device__ __forceinline__ void fetch(const Rows<T> &o, int64_t row0, int col, int lane) {
+    const int c = col + lane % PIECES * E;
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c) w[c] = in ? p[c] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < PIECES; ++i) {
+      const int64_t row = row0 + i * (32 / PIECES) + lane / PIECES;
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (row >= o.M) continue;
+      const T *p = o.p + row * o.ld + c;
+      if (o.vec && c + E <= o.N) {
+        w[i] = *reinterpret_cast<const uint4 *>(p);
+      } else {
+        float v[E];
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c) unpack16<T>(w[c], v + c * E);
-    return;
+        for (int k = 0; k < E; ++k) v[k] = c + k < o.N ? to_f32(p[k]) : 0.0f;
+        w[i] = pack16<T>(v);
+      }
+    }
   }
-  T *e = reinterpret_cast<T *>(stg);
-  const int rows = (int)max((int64_t)0, min((int64_t)32, o.M - row0));
-  T zero;
-  from_f32(zero, 0.0f);
-  for (int r = 0; r < 32; ++r)
-    e[stg_at<T>(r, lane / E) * E + lane % E] =
-        r < rows && col + lane < o.N ? o.p[(row0 + r) * o.ld + col + lane] : zero;
-  __syncwarp();
-  const uint4 *s = reinterpret_cast<const uint4 *>(stg);
+  __device__ __forceinline__ void get(float (&v)[32], uint8_t *stg, int lane) const {
+    uint4 *s = reinterpret_cast<uint4 *>(stg);
 #pragma unroll
-  for (int c = 0; c < PIECES; ++c) unpack16<T>(s[stg_at<T>(lane, c)], v + c * E);
-  __syncwarp();
-}
+    for (int i = 0; i < PIECES; ++i) s[stg_at<T>(i * (32 / PIECES) + lane / PIECES, lane % PIECES)] = w[i];
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < PIECES; ++c) unpack16<T>(s[stg_at<T>(lane, c)], v + c * E);
+    __syncwarp();
+  }
+};
 
 __device__ __forceinline__ void acc32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
@@ -202,67 +196,96 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const float *bias) {
   }
 }
 
-// This warp's 32 rows (row0 ...) x the tile's output columns (col0 ...) from
-// the accumulator at taddr.  sb: the tile's bias columns in shared memory.
+// This warp's 32 rows (row0 ...) x columns [c0, c1) of the tile's output
+// columns (the tile's first is col0) from the accumulator at taddr.  sb: the
+// bias of those columns in shared memory (gated: W1's, then W3's).  What the
+// epilogue reads from global memory does not depend on the accumulator: each
+// chunk's is fetched a chunk ahead, the first (begin) before the wait for
+// the accumulator.
 template <int EPI, typename T>
-__device__ __forceinline__ void epilogue(const TcParams &P, const TcProblem &Q, uint32_t taddr, int64_t row0,
-                                         int col0, const float *sb, uint8_t *stg, int lane) {
-  constexpr bool FAST = sizeof(T) == 2;
-  const Rows<T> out(Q.out, Q.ld_o, Q.M, Q.N);
-  if (row0 >= Q.M) return;
-  for (int c = 0; c < P.bnh && col0 + c < Q.N; c += 32) {
-    float v[32];
-    acc32(taddr + c, v);
-    const int col = col0 + c;
-    if (EPI == kDenseStore) {
-      store32(out, row0, col, v, stg, lane);
-    } else if (EPI == kDenseLinear) {
-      if (Q.bias) add_bias(v, sb + c);
-      if (Q.pre) store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
-      if (P.act != MOE_DENSE_IDENTITY) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act);
-      }
-      if (Q.residual) {
-        float r[32];
-        load32(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col, r, stg, lane);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += r[i];
-      }
-      store32(out, row0, col, v, stg, lane);
-    } else if (EPI == kDenseGated) {
-      float u[32];
-      acc32(taddr + P.bnh + c, u);
-      if (Q.bias) {
-        add_bias(v, sb + c);
-        add_bias(u, sb + P.bnh + c);
-      }
-      if (Q.pre) {
-        store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
-        store32(Rows<T>(Q.pre3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act) * u[i];
-      store32(out, row0, col, v, stg, lane);
-    } else {                                             // kDenseGatedGrad
-      float a[32], u[32];
-      load32(Rows<T>(Q.pre_in, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
-      load32(Rows<T>(Q.pre3_in, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float f, d;
-        act_both<FAST>(a[i], P.act, f, d);
-        const float dh = v[i];
-        v[i] = dh * u[i] * d;
-        a[i] = dh * f;
-        u[i] = f * u[i];
-      }
-      store32(out, row0, col, v, stg, lane);
-      store32(Rows<T>(Q.out2, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
-      store32(Rows<T>(Q.out3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+struct Epilogue {
+  static constexpr bool FAST = sizeof(T) == 2;
+  static constexpr int kIn = EPI == kDenseGatedGrad ? 2 : 1;
+  const TcParams &P;
+  const TcProblem &Q;
+  const int64_t row0;
+  const int col0, c0, c1, lane;
+  uint8_t *stg;
+  Piece32<T> in[kIn];
+
+  __device__ Epilogue(const TcParams &p, const TcProblem &q, int64_t row, int col, int a, int b, uint8_t *st, int l)
+      : P(p), Q(q), row0(row), col0(col), c0(a), c1(min(b, q.N - col)), lane(l), stg(st) {}
+
+  __device__ __forceinline__ void fetch(int c) {
+    if (row0 >= Q.M || c >= c1) return;
+    if (EPI == kDenseLinear && Q.residual)
+      in[0].fetch(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col0 + c, lane);
+    if (EPI == kDenseGatedGrad) {
+      in[0].fetch(Rows<T>(Q.pre_in, Q.N, Q.M, Q.N), row0, col0 + c, lane);
+      in[kIn - 1].fetch(Rows<T>(Q.pre3_in, Q.N, Q.M, Q.N), row0, col0 + c, lane);
     }
   }
-}
+  __device__ __forceinline__ void begin() { fetch(c0); }
+
+  __device__ __forceinline__ void run(uint32_t taddr, const float *sb) {
+    if (row0 >= Q.M) return;
+    const Rows<T> out(Q.out, Q.ld_o, Q.M, Q.N);
+    for (int c = c0; c < c1; c += 32) {
+      float v[32];
+      acc32(taddr + c, v);
+      const int col = col0 + c;
+      if (EPI == kDenseStore) {
+        store32(out, row0, col, v, stg, lane);
+      } else if (EPI == kDenseLinear) {
+        if (Q.bias) add_bias(v, sb + c - c0);
+        if (Q.pre) store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
+        if (P.act != MOE_DENSE_IDENTITY) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act);
+        }
+        if (Q.residual) {
+          float r[32];
+          in[0].get(r, stg, lane);
+          fetch(c + 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] += r[i];
+        }
+        store32(out, row0, col, v, stg, lane);
+      } else if (EPI == kDenseGated) {
+        float u[32];
+        acc32(taddr + P.bnh + c, u);
+        if (Q.bias) {
+          add_bias(v, sb + c - c0);
+          add_bias(u, sb + kAccCols / 4 + c - c0);
+        }
+        if (Q.pre) {
+          store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
+          store32(Rows<T>(Q.pre3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act) * u[i];
+        store32(out, row0, col, v, stg, lane);
+      } else {                                           // kDenseGatedGrad
+        float a[32], u[32];
+        in[0].get(a, stg, lane);
+        in[kIn - 1].get(u, stg, lane);
+        fetch(c + 32);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float f, d;
+          act_both<FAST>(a[i], P.act, f, d);
+          const float dh = v[i];
+          v[i] = dh * u[i] * d;
+          a[i] = dh * f;
+          u[i] = f * u[i];
+        }
+        store32(out, row0, col, v, stg, lane);
+        store32(Rows<T>(Q.out2, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
+        store32(Rows<T>(Q.out3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+      }
+    }
+  }
+};
 
 // --------------------------------- the kernel ----------------------------------
 template <int EPI, bool AMN, bool BMN, typename T>
@@ -274,14 +297,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t accf_bar[2];
   __shared__ __align__(8) uint64_t acce_bar[2];
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ __align__(16) float s_bias[4][kAccCols];       // a copy for each epilogue warp
+  __shared__ __align__(16) float s_bias[kEpiWarps][kAccCols / 2];     // each epilogue warp's columns
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   __shared__ uint64_t s_limit_sh;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t b_bytes = (uint32_t)(P.bn / 2) * BK * 2;
-  const uint32_t stage_bytes = kABytes + b_bytes;
+  const uint32_t stage_bytes = kBks * (kABytes + b_bytes);       // A blocks, then B blocks
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -294,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf_bar[a], 1);
-      mbar_init(&acce_bar[a], 2 * 4 * 32);
+      mbar_init(&acce_bar[a], 2 * kEpiWarps * 32);
     }
     mbar_init(&drain_bar, 1);
     s_abort = 0;
@@ -333,26 +356,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Seg S = P.seg[sg];
         const CUtensorMap *ma = &Q.a[S.a];
         const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
-        for (int kb = 0; kb < Q.KB; ++kb) {
+        for (int kb = 0; kb < Q.KB; kb += kBks) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) { ok = false; break; }
           uint8_t *sa = smem + (size_t)stage * stage_bytes;
-          uint8_t *sb = sa + kABytes;
+          uint8_t *sb = sa + kBks * kABytes;
           const uint32_t fb = smem_u32(&full_bar[stage]) & 0xFEFFFFFFu;      // the even CTA's barrier
+          const int nq = min(kBks, Q.KB - kb);
           if (rank == 0) {
-            mbar_expect_tx(&full_bar[stage], 2 * stage_bytes);
+            mbar_expect_tx(&full_bar[stage], 2 * nq * (kABytes + b_bytes));
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
           }
-          if (AMN) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tma_load_3d_pair(sa + j * 8192, ma, fb, am + j * 64, kb * BK, S.az);
-          } else {
-            tma_load_3d_pair(sa, ma, fb, kb * BK, am, S.az);
-          }
-          // 64-line boxes (8 KB) either way: one or two of them are this CTA's half
-          for (int j = 0; j < P.bn / 128; ++j) {
-            if (BMN) tma_load_3d_pair(sb + j * 8192, mb, fb, bn0 + j * 64, kb * BK, S.bz);
-            else tma_load_3d_pair(sb + j * 8192, mb, fb, kb * BK, bn0 + j * 64, S.bz);
+          for (int q2 = 0; q2 < nq; ++q2) {
+            const int k = (kb + q2) * BK;
+            if (AMN) {
+              tma_load_3d_pair(sa, ma, fb, am, k, S.az);
+              tma_load_3d_pair(sa + 8192, ma, fb, am + 64, k, S.az);
+            } else {
+              tma_load_3d_pair(sa, ma, fb, k, am, S.az);
+            }
+            if (BMN) {
+              tma_load_3d_pair(sb, mb, fb, bn0, k, S.bz);
+              if (P.bn == 256) tma_load_3d_pair(sb + 8192, mb, fb, bn0 + 64, k, S.bz);
+            } else {
+              tma_load_3d_pair(sb, mb, fb, k, bn0, S.bz);
+            }
+            sa += kABytes;
+            sb += b_bytes;
           }
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
@@ -369,22 +399,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += npairs) {
-      const int nkb = P.segs * P.pr[tile_pos(P, t).p].KB;
+      const int KB = P.pr[tile_pos(P, t).p].KB;
       if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
-      for (int kb = 0; kb < nkb; ++kb) {
-        if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t a_addr = smem_u32(smem + (size_t)stage * stage_bytes);
-        const uint32_t b_addr = a_addr + kABytes;
+      uint32_t accum = 0;
+      for (int sg = 0; ok && sg < P.segs; ++sg) {
+        for (int kb = 0; kb < KB; kb += kBks) {
+          if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes);
+          const int nq = min(kBks, KB - kb);
+          for (int q2 = 0; q2 < nq; ++q2) {
+            const uint32_t a_addr = a0 + q2 * kABytes, b_addr = a0 + kBks * kABytes + q2 * b_bytes;
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          umma_bf16_pair(d_tmem, AMN ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
-                         BMN ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc,
-                         (kb > 0 || k > 0) ? 1u : 0u);
-        umma_commit_pair_both(&empty_bar[stage]);
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            for (int k = 0; k < BK / 16; ++k) {
+              umma_bf16_pair(d_tmem, AMN ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
+                             BMN ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc, accum);
+              accum = 1;
+            }
+          }
+          umma_commit_pair_both(&empty_bar[stage]);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        }
       }
       if (!ok) break;
       umma_commit_pair_both(&accf_bar[acc]);
@@ -394,27 +431,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_wait_drain(&drain_bar, 0);
   } else if (warp >= 4) {
     // -------------------------------- epilogue --------------------------------
-    const int ew = warp - 4;
-    uint8_t *stg = smem + (size_t)kStages * stage_bytes + (size_t)ew * kStagePerWarp;
+    // two warps a TMEM lane quarter (a warp reaches lanes 32 (warp mod 4) ...
+    // of its CTA only), each with half of the tile's columns
+    const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+    uint8_t *stg = smem + (size_t)kStages * stage_bytes + (size_t)ew * (32 * 32 * sizeof(T));
     const uint32_t acce_even[2] = {mapa_shared(smem_u32(&acce_bar[0]), 0), mapa_shared(smem_u32(&acce_bar[1]), 0)};
+    float *sb = s_bias[ew];
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = pair; t < tiles; t += npairs) {
       const TilePos q = tile_pos(P, t);
       const TcProblem &Q = P.pr[q.p];
-      const int col0 = q.n * P.bnh;
+      const int col0 = q.n * P.bnh, w = P.bnh / 2;
       if ((EPI == kDenseLinear || EPI == kDenseGated) && Q.bias) {
-        for (int i = lane; i < P.bn; i += 32) {
-          const bool up = EPI == kDenseGated && i >= P.bnh;
-          const int n = col0 + (up ? i - P.bnh : i);
-          s_bias[ew][i] = n < Q.N ? to_f32(static_cast<const T *>(up ? Q.bias3 : Q.bias)[n]) : 0.0f;
+        for (int i = lane; i < w; i += 32) {
+          const int n = col0 + half * w + i;
+          sb[i] = n < Q.N ? to_f32(static_cast<const T *>(Q.bias)[n]) : 0.0f;
+          if (EPI == kDenseGated)
+            sb[kAccCols / 4 + i] = n < Q.N ? to_f32(static_cast<const T *>(Q.bias3)[n]) : 0.0f;
         }
         __syncwarp();
       }
+      Epilogue<EPI, T> ep(P, Q, (int64_t)q.m * 2 * BM + rank * BM + quarter * 32, col0, half * w, half * w + w, stg,
+                          lane);
+      ep.begin();
       if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit))) break;
       tc_fence_after();
-      epilogue<EPI, T>(P, Q, tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(ew * 32) << 16),
-                       (int64_t)q.m * 2 * BM + rank * BM + ew * 32, col0, s_bias[ew], stg, lane);
+      ep.run(tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(quarter * 32) << 16), sb);
       __syncwarp();
       tc_fence_before();
       mbar_arrive_cluster(acce_even[acc]);
@@ -459,33 +502,19 @@ cudaError_t pairs_of(size_t smem, int *pairs) {
   return cudaSuccess;
 }
 
-constexpr size_t kSmemBytes = 1024 + kStages * (kABytes + 128 * BK * 2) + 4 * kStagePerWarp;
+template <typename T>
+constexpr size_t smem_bytes() {
+  return 1024 + kStages * kBks * (kABytes + 128 * BK * 2) + kEpiWarps * 32 * 32 * sizeof(T);
+}
 
 template <int EPI, bool AMN, bool BMN, typename T>
-cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
+cudaError_t launch_pair_as(const TcParams &P, cudaStream_t s) {
   constexpr auto kern = dense_pair_kernel<EPI, AMN, BMN, T>;
   int pairs = 0;
-  cudaError_t e = pairs_of<kern>(kSmemBytes, &pairs);
+  const cudaError_t e = pairs_of<kern>(smem_bytes<T>(), &pairs);
   if (e != cudaSuccess) return e;
-  // columns of a tile: the width whose last wave wastes less (a 128-column
-  // tile costs about 0.55 of a 256-column one)
-  auto waves = [&](int bn) {
-    int64_t tiles = 0;
-    for (int p = 0; p < P.nprob; ++p) {
-      const int bnh = EPI == kDenseGated ? bn / 2 : bn;
-      tiles += (int64_t)P.pr[p].tiles_m * ((P.pr[p].N + bnh - 1) / bnh);
-    }
-    return (double)((tiles + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55);
-  };
-  P.bn = waves(128) < waves(256) ? 128 : 256;
-  P.bnh = EPI == kDenseGated ? P.bn / 2 : P.bn;
-  int64_t end = 0;
-  for (int p = 0; p < P.nprob; ++p) {
-    end += (int64_t)P.pr[p].tiles_m * ((P.pr[p].N + P.bnh - 1) / P.bnh);
-    if (end > 0x3fffffff) return cudaErrorInvalidValue;
-    P.pr[p].tile_end = (int32_t)end;
-  }
-  return launch_kernel(kern, 2 * (unsigned)std::min<int64_t>(pairs, end), kThreads, kSmemBytes, s, P);
+  return launch_kernel(kern, 2 * (unsigned)std::min<int>(pairs, P.pr[P.nprob - 1].tile_end), kThreads,
+                       smem_bytes<T>(), s, P);
 }
 
 bool kmajor(const Operand &o) { return o.ks == 1; }
@@ -531,23 +560,38 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
   P.nprob = n;
   P.segs = g[0].a2.p ? 2 : 1;
   for (int i = 0; i < P.segs; ++i) P.seg[i] = {(uint8_t)i, 0, (uint8_t)i, 0};
-  // the boxes' height depends on the tile width, which launch_pair_as picks;
-  // both widths are a multiple of 64, so maps of 64-line boxes serve K-major
-  // B of 128 columns and two loads of them the 256-column tile
+  // columns of a tile: the width whose last wave wastes less (a 128-column
+  // tile costs about 0.55 of a 256-column one)
+  const bool gated = g[0].epi == kDenseGated;
+  const int pairs = std::max(1, device_sms() / 2);
+  auto tiles_at = [&](int bn, int upto) {
+    int64_t t = 0;
+    for (int p = 0; p < upto; ++p) {
+      const int w = gated ? bn / 2 : bn;
+      t += ((g[p].M + 2 * BM - 1) / (2 * BM)) * ((g[p].N + w - 1) / w);
+    }
+    return t;
+  };
+  auto cost = [&](int bn) { return (double)((tiles_at(bn, n) + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55); };
+  P.bn = cost(128) < cost(256) ? 128 : 256;
+  P.bnh = gated ? P.bn / 2 : P.bn;
+  if (tiles_at(P.bn, n) > 0x3fffffff) return cudaErrorInvalidValue;
+  auto box_b = [&](const Operand &o) { return kmajor(o) ? P.bn / 2 : BK; };
   for (int p = 0; p < n; ++p) {
     TcProblem &Q = P.pr[p];
     const DenseGemm &G = g[p];
     bool ok = map_operand(&Q.a[0], G.a, G.M, G.K, kmajor(G.a) ? BM : BK, 1, 0) &&
-              map_operand(&Q.b[0], G.b, G.N, G.K, BK, 1, 0);
+              map_operand(&Q.b[0], G.b, G.N, G.K, box_b(G.b), 1, 0);
     if (G.a2.p)
       ok = ok && map_operand(&Q.a[1], G.a2, G.M, G.K, kmajor(G.a2) ? BM : BK, 1, 0) &&
-           map_operand(&Q.b[1], G.b2, G.N, G.K, BK, 1, 0);
-    if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, BK, 1, 0);
+           map_operand(&Q.b[1], G.b2, G.N, G.K, box_b(G.b2), 1, 0);
+    if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, box_b(G.b3), 1, 0);
     if (!ok) return cudaErrorInvalidValue;
     Q.M = G.M;
     Q.N = G.N;
     Q.KB = (int32_t)((G.K + BK - 1) / BK);
     Q.tiles_m = (int32_t)((G.M + 2 * BM - 1) / (2 * BM));
+    Q.tile_end = (int32_t)tiles_at(P.bn, p + 1);
     Q.bias = G.bias;
     Q.bias3 = G.bias3;
     Q.residual = G.residual;
