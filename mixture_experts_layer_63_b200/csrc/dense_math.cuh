@@ -47,49 +47,57 @@ __device__ __forceinline__ float sigmoid_t(float v) {
 constexpr float kGeluA = 0.7978845608028654f;       // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// act(v).  A NaN stays a NaN (relu compares instead of taking a maximum).
-template <bool FAST>
-__device__ __forceinline__ float act_fwd(float v, int act) {
+// Call f with the activation as a compile-time constant: one branch for a
+// whole row of elements (a switch an element, unrolled, cost more in branches
+// and instruction fetches than the functions themselves: the gradient
+// epilogue of 4096 x 2048 x 5632 took 192 us with it, against a 60 us product).
+template <int V>
+struct IntC {
+  static constexpr int value = V;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
-    case MOE_DENSE_RELU: return v < 0.0f ? 0.0f : v;
-    case MOE_DENSE_SILU: return FAST ? __fdividef(v, 1.0f + __expf(-v)) : v / (1.0f + expf(-v));
-    case MOE_DENSE_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case MOE_DENSE_GELU_TANH:
-      return v * sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
-    default: return v;
+    case MOE_DENSE_RELU: f(IntC<MOE_DENSE_RELU>{}); break;
+    case MOE_DENSE_SILU: f(IntC<MOE_DENSE_SILU>{}); break;
+    case MOE_DENSE_GELU: f(IntC<MOE_DENSE_GELU>{}); break;
+    case MOE_DENSE_GELU_TANH: f(IntC<MOE_DENSE_GELU_TANH>{}); break;
+    default: f(IntC<MOE_DENSE_IDENTITY>{});
   }
 }
 
+// act(v).  A NaN stays a NaN (relu compares instead of taking a maximum).
+template <bool FAST, int ACT>
+__device__ __forceinline__ float act_fwd(float v) {
+  if (ACT == MOE_DENSE_RELU) return v < 0.0f ? 0.0f : v;
+  if (ACT == MOE_DENSE_SILU) return FAST ? __fdividef(v, 1.0f + __expf(-v)) : v / (1.0f + expf(-v));
+  if (ACT == MOE_DENSE_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (ACT == MOE_DENSE_GELU_TANH) return v * sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
+  return v;
+}
+
 // act(v) and act'(v); relu'(0) = 0, as in the MoE layer's backward pass
-template <bool FAST>
-__device__ __forceinline__ void act_both(float v, int act, float &f, float &d) {
-  switch (act) {
-    case MOE_DENSE_RELU:
-      f = v < 0.0f ? 0.0f : v;
-      d = v > 0.0f ? 1.0f : 0.0f;
-      break;
-    case MOE_DENSE_SILU: {
-      const float s = sigmoid_t<FAST>(v);
-      f = v * s;
-      d = s * (1.0f + v * (1.0f - s));
-      break;
-    }
-    case MOE_DENSE_GELU: {
-      const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));      // normal CDF
-      const float p = 0.3989422804014327f * (FAST ? __expf(-0.5f * v * v) : expf(-0.5f * v * v));
-      f = v * c;
-      d = c + v * p;
-      break;
-    }
-    case MOE_DENSE_GELU_TANH: {
-      const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
-      f = v * s;
-      d = s + v * s * (1.0f - s) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * v * v);
-      break;
-    }
-    default:
-      f = v;
-      d = 1.0f;
+template <bool FAST, int ACT>
+__device__ __forceinline__ void act_both(float v, float &f, float &d) {
+  if (ACT == MOE_DENSE_RELU) {
+    f = v < 0.0f ? 0.0f : v;
+    d = v > 0.0f ? 1.0f : 0.0f;
+  } else if (ACT == MOE_DENSE_SILU) {
+    const float s = sigmoid_t<FAST>(v);
+    f = v * s;
+    d = s * (1.0f + v * (1.0f - s));
+  } else if (ACT == MOE_DENSE_GELU) {
+    const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));      // normal CDF
+    const float p = 0.3989422804014327f * (FAST ? __expf(-0.5f * v * v) : expf(-0.5f * v * v));
+    f = v * c;
+    d = c + v * p;
+  } else if (ACT == MOE_DENSE_GELU_TANH) {
+    const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
+    f = v * s;
+    d = s + v * s * (1.0f - s) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * v * v);
+  } else {
+    f = v;
+    d = 1.0f;
   }
 }
 

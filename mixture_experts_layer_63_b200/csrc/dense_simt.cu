@@ -45,7 +45,8 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
   switch (P.epi) {
     case kDenseLinear: {
       const float z = P.bias ? acc + to_f32(static_cast<const T *>(P.bias)[n]) : acc;
-      float y = act_fwd<FAST>(z, P.act);
+      float y = 0.0f;
+      with_act(P.act, [&](auto A) { y = act_fwd<FAST, decltype(A)::value>(z); });
       if (P.residual) y += to_f32(static_cast<const T *>(P.residual)[m * P.ld_r + n]);
       if (P.pre) from_f32(static_cast<T *>(P.pre)[at], z);
       from_f32(*out, y);
@@ -56,14 +57,16 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
       const float u = P.bias3 ? acc3 + to_f32(static_cast<const T *>(P.bias3)[n]) : acc3;
       if (P.pre) from_f32(static_cast<T *>(P.pre)[at], a);
       if (P.pre3) from_f32(static_cast<T *>(P.pre3)[at], u);
-      from_f32(*out, act_fwd<FAST>(a, P.act) * u);
+      float f = 0.0f;
+      with_act(P.act, [&](auto A) { f = act_fwd<FAST, decltype(A)::value>(a); });
+      from_f32(*out, f * u);
       break;
     }
     case kDenseGatedGrad: {
       const float a = to_f32(static_cast<const T *>(P.pre_in)[at]);
       const float u = to_f32(static_cast<const T *>(P.pre3_in)[at]);
-      float f, d;
-      act_both<FAST>(a, P.act, f, d);
+      float f = 0.0f, d = 0.0f;
+      with_act(P.act, [&](auto A) { act_both<FAST, decltype(A)::value>(a, f, d); });
       from_f32(*out, acc * u * d);
       from_f32(static_cast<T *>(P.out2)[at], acc * f);
       from_f32(static_cast<T *>(P.out3)[at], f * u);
@@ -135,15 +138,16 @@ __global__ void __launch_bounds__(256) dense_simt_kernel(const DenseGemm P) {
 // eight interleaved, and leaves their sums in part[y][n]; the second kernel
 // adds the parts in order.  dz enters its sums before its rounding.  No
 // atomics: the same bits on every call.
+constexpr int kNoAct = -1;
 struct ColSums {
   ColSum q[kMaxColSums];
   int64_t M;
-  int parts, act;
+  int parts;
   float *part;                 // [count][parts][max N]
   int64_t part_stride;
 };
 
-template <typename T, bool ACT>
+template <typename T, int ACT>          // ACT: the activation, or kNoAct
 __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
   constexpr int V = 16 / sizeof(T);
   __shared__ float red[8][32 * V];
@@ -159,7 +163,8 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
   T *dz = static_cast<T *>(Q.dz);
   float sum[V] = {};
   uintptr_t at = reinterpret_cast<uintptr_t>(src) | (uintptr_t)(Q.ld * (int64_t)sizeof(T));
-  if (ACT) at |= reinterpret_cast<uintptr_t>(z) | (uintptr_t)((int64_t)Q.N * sizeof(T));
+  constexpr bool GRAD = ACT != kNoAct;
+  if (GRAD) at |= reinterpret_cast<uintptr_t>(z) | (uintptr_t)((int64_t)Q.N * sizeof(T));
   const int n = n0 + lane * V;
   if ((at & 15) == 0 && n0 + 32 * V <= Q.N) {
     // whole 16-byte pieces, four rows in flight
@@ -170,20 +175,20 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
       for (int i = 0; i < R; ++i)
         if (r + 8 * i < r1) {
           a[i] = *reinterpret_cast<const uint4 *>(src + (r + 8 * i) * Q.ld + n);
-          if (ACT) b[i] = *reinterpret_cast<const uint4 *>(z + (r + 8 * i) * Q.N + n);
+          if (GRAD) b[i] = *reinterpret_cast<const uint4 *>(z + (r + 8 * i) * Q.N + n);
         }
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         if (r + 8 * i >= r1) break;
         float v[V];
         unpack16<T>(a[i], v);
-        if (ACT) {
+        if (GRAD) {
           float zz[V];
           unpack16<T>(b[i], zz);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
             float f, d;
-            act_both<sizeof(T) == 2>(zz[j], P.act, f, d);
+            act_both<sizeof(T) == 2, ACT>(zz[j], f, d);
             v[j] *= d;
           }
           *reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.N + n) = pack16<T>(v);
@@ -200,9 +205,9 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
         const int c = n0 + 32 * j + lane;
         if (c >= Q.N) break;
         float v = to_f32(src[r * Q.ld + c]);
-        if (ACT) {
+        if (GRAD) {
           float f, d;
-          act_both<sizeof(T) == 2>(to_f32(z[r * Q.N + c]), P.act, f, d);
+          act_both<sizeof(T) == 2, ACT>(to_f32(z[r * Q.N + c]), f, d);
           v *= d;
           from_f32(dz[r * Q.N + c], v);
         }
@@ -242,11 +247,18 @@ int colsum_parts(int64_t M, int N) {
 }
 
 template <typename T>
-cudaError_t colsums_as(const ColSums &P, int count, int maxN, bool act, bool join, cudaStream_t s) {
+cudaError_t colsums_as(const ColSums &P, int count, int maxN, int act, bool join, cudaStream_t s) {
   constexpr int W = 32 * (16 / sizeof(T));
   const dim3 grid((maxN + W - 1) / W, P.parts, count);
-  const cudaError_t e = act ? launch_kernel(colsum_part_kernel<T, true>, grid, 256, 0, s, P)
-                            : launch_kernel(colsum_part_kernel<T, false>, grid, 256, 0, s, P);
+  auto run = [&](auto kern) { return launch_kernel(kern, grid, 256, 0, s, P); };
+  cudaError_t e;
+  switch (act) {
+    case MOE_DENSE_RELU: e = run(colsum_part_kernel<T, MOE_DENSE_RELU>); break;
+    case MOE_DENSE_SILU: e = run(colsum_part_kernel<T, MOE_DENSE_SILU>); break;
+    case MOE_DENSE_GELU: e = run(colsum_part_kernel<T, MOE_DENSE_GELU>); break;
+    case MOE_DENSE_GELU_TANH: e = run(colsum_part_kernel<T, MOE_DENSE_GELU_TANH>); break;
+    default: e = run(colsum_part_kernel<T, kNoAct>);
+  }
   if (e != cudaSuccess || !join) return e;
   return launch_kernel(colsum_join_kernel<T>, dim3((maxN + 255) / 256, 1, count), 256, 0, s, P);
 }
@@ -283,12 +295,11 @@ cudaError_t launch_colsums(int act, int dtype, int64_t M, const ColSum *q, int c
     join = join || q[i].out;
   }
   P.M = M;
-  P.act = act;
   P.parts = colsum_parts(M, maxN);
   P.part = part;
   P.part_stride = maxN;
-  return dtype == MOE_F32 ? colsums_as<float>(P, count, maxN, grad, join, s)
-                          : colsums_as<__nv_bfloat16>(P, count, maxN, grad, join, s);
+  return dtype == MOE_F32 ? colsums_as<float>(P, count, maxN, grad ? act : kNoAct, join, s)
+                          : colsums_as<__nv_bfloat16>(P, count, maxN, grad ? act : kNoAct, join, s);
 }
 
 }  // namespace moe

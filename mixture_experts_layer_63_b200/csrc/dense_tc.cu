@@ -239,10 +239,10 @@ struct Epilogue {
       } else if (EPI == kDenseLinear) {
         if (Q.bias) add_bias(v, sb + c - c0);
         if (Q.pre) store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
-        if (P.act != MOE_DENSE_IDENTITY) {
+        with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act);
-        }
+          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]);
+        });
         if (Q.residual) {
           float r[32];
           in[0].get(r, stg, lane);
@@ -262,23 +262,27 @@ struct Epilogue {
           store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
           store32(Rows<T>(Q.pre3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
         }
+        with_act(P.act, [&](auto A) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST>(v[i], P.act) * u[i];
+          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]) * u[i];
+        });
         store32(out, row0, col, v, stg, lane);
       } else {                                           // kDenseGatedGrad
         float a[32], u[32];
         in[0].get(a, stg, lane);
         in[kIn - 1].get(u, stg, lane);
         fetch(c + 32);
+        with_act(P.act, [&](auto A) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float f, d;
-          act_both<FAST>(a[i], P.act, f, d);
-          const float dh = v[i];
-          v[i] = dh * u[i] * d;
-          a[i] = dh * f;
-          u[i] = f * u[i];
-        }
+          for (int i = 0; i < 32; ++i) {
+            float f, d;
+            act_both<FAST, decltype(A)::value>(a[i], f, d);
+            const float dh = v[i];
+            v[i] = dh * u[i] * d;
+            a[i] = dh * f;
+            u[i] = f * u[i];
+          }
+        });
         store32(out, row0, col, v, stg, lane);
         store32(Rows<T>(Q.out2, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
         store32(Rows<T>(Q.out3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
