@@ -125,6 +125,21 @@ cudaError_t run_products(const DenseGemm *g, int n, char *ws, cudaStream_t s) {
   for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_dense_simt(g[i], s);
   return e;
 }
+// out [M, N] = sum over k < K of a(m, k) b(n, k)
+DenseGemm product(int dtype, int64_t M, int64_t K, int32_t N, const Operand &a, const Operand &b, void *out,
+                  int64_t ld_o) {
+  DenseGemm g{};
+  g.epi = kDenseStore;
+  g.dtype = dtype;
+  g.M = M;
+  g.K = K;
+  g.N = N;
+  g.a = a;
+  g.b = b;
+  g.out = out;
+  g.ld_o = ld_o;
+  return g;
+}
 cudaError_t run_product(const DenseGemm &g, char *ws, cudaStream_t s) { return run_products(&g, 1, ws, s); }
 
 // ---- gated block ------------------------------------------------------------------
@@ -238,29 +253,11 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
     e = launch_colsums(c.act, c.dtype, c.M, &q, 1, reinterpret_cast<float *>(base + L.part), s);
     if (act) dz = {base + L.dz, c.N, 1};
   }
-  DenseGemm g{};
-  g.epi = kDenseStore;
-  g.dtype = c.dtype;
-  if (e == cudaSuccess && dx && c.M > 0) {
-    g.M = c.M;
-    g.N = c.K;
-    g.K = c.N;
-    g.a = dz;
-    g.b = {w, 1, c.ld_w};                   // W [N, K] contracted over its rows
-    g.out = dx;
-    g.ld_o = c.ld_x;
-    e = run_product(g, base, s);
-  }
-  if (e == cudaSuccess && dw) {
-    g.M = c.N;
-    g.N = c.K;
-    g.K = c.M;
-    g.a = {dz.p, 1, dz.rs};                 // both operands contracted over the rows
-    g.b = {x, 1, c.ld_x};
-    g.out = dw;
-    g.ld_o = c.K;
-    e = run_product(g, base, s);
-  }
+  DenseGemm g[2] = {};
+  int n = 0;
+  if (dx && c.M > 0) g[n++] = product(c.dtype, c.M, c.N, c.K, dz, {w, 1, c.ld_w}, dx, c.ld_x);
+  if (dw) g[n++] = product(c.dtype, c.N, c.M, c.K, {dz.p, 1, dz.rs}, {x, 1, c.ld_x}, dw, c.K);
+  if (e == cudaSuccess && n > 0) e = run_products(g, n, base, s);
   return dense_status(e);
 }
 
@@ -376,40 +373,20 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
     g.out3 = h;
     e = run_product(g, base, s);
   }
-  DenseGemm g{};
-  g.epi = kDenseStore;
-  g.dtype = c.dtype;
-  if (e == cudaSuccess && dx && T > 0) {
-    DenseGemm q = g;
-    q.M = T;
-    q.N = c.d_model;
-    q.K = f;
-    q.a = {da, f, 1};
-    q.b = {w1, 1, d};
-    q.a2 = {du, f, 1};
-    q.b2 = {w3, 1, d};
-    q.out = dx;
-    q.ld_o = c.ld_x;
-    e = run_product(q, base, s);
+  // dx and the weight gradients (each contracts two matrices over the rows) in one launch
+  DenseGemm g[4] = {};
+  int n = 0;
+  if (dx && T > 0) {
+    g[n] = product(c.dtype, T, f, c.d_model, {da, f, 1}, {w1, 1, d}, dx, c.ld_x);
+    g[n].a2 = {du, f, 1};
+    g[n++].b2 = {w3, 1, d};
   }
-  // weight gradients [M, N] = left^T right, contracted over the rows: one launch
-  g.K = T;
-  DenseGemm wg[3];
-  int nw = 0;
-  auto wgrad = [&](const void *l, int64_t ld_l, int64_t M, const void *r, int64_t ld_r, int32_t N, void *out) {
-    if (!out) return;
-    g.M = M;
-    g.N = N;
-    g.a = {l, 1, ld_l};
-    g.b = {r, 1, ld_r};
-    g.out = out;
-    g.ld_o = N;
-    wg[nw++] = g;
-  };
-  wgrad(da, f, f, x, c.ld_x, c.d_model, dw1);
-  wgrad(du, f, f, x, c.ld_x, c.d_model, dw3);
-  wgrad(dy, c.ld_y, d, h, f, c.d_ff, dw2);
-  if (e == cudaSuccess && nw > 0) e = run_products(wg, nw, base, s);
+  if (dw1) {
+    g[n++] = product(c.dtype, f, T, c.d_model, {da, 1, f}, {x, 1, c.ld_x}, dw1, d);
+    g[n++] = product(c.dtype, f, T, c.d_model, {du, 1, f}, {x, 1, c.ld_x}, dw3, d);
+  }
+  if (dw2) g[n++] = product(c.dtype, d, T, c.d_ff, {dy, 1, c.ld_y}, {h, 1, f}, dw2, f);
+  if (e == cudaSuccess && n > 0) e = run_products(g, n, base, s);
   ColSum bq[3];
   int nb = 0;
   if (db1) bq[nb++] = {da, f, c.d_ff, nullptr, nullptr, db1};

@@ -48,8 +48,8 @@ inline size_t dense_elem(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 
 // Tensor-core products (dense_tc.cu).  dense_tc_ok: bf16 operands whose base
-// and lines are 16-byte aligned.  launch_dense_tc runs up to three products of
-// one kind (same epilogue, same operand orders) in one launch.
+// and lines are 16-byte aligned.  launch_dense_tc runs up to four products with
+// one epilogue in one launch.
 bool dense_tc_ok(const DenseGemm &g);
 cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
 

@@ -47,6 +47,28 @@ __device__ __forceinline__ float sigmoid_t(float v) {
 constexpr float kGeluA = 0.7978845608028654f;       // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
+// Normal distribution function for the bf16 layers' GELU, and e^(-v^2/2) on
+// the way: Phi(-x) = e^(-x^2/2) t Q(t), t = 1 / (1 + x / (2 sqrt 2)), x >= 0,
+// where t Q(t) is a degree-7 polynomial fitted (weighted least squares to a
+// minimax error, float64) to half the scaled complementary error function of
+// x / sqrt 2 on [0, 17]; relative error 2.4e-6 in fp32, in the tail too.
+// Against erff and a second exponential: the column-sum pass over 4096 x 4096
+// went from 33 to 23 us.
+__device__ __forceinline__ float normal_cdf_fast(float v, float &e) {
+  const float x = fabsf(v);
+  e = __expf(-0.5f * v * v);
+  const float t = __fdividef(1.0f, fmaf(0.35355339f, x, 1.0f));
+  float q = 0.042448815f;
+  q = fmaf(q, t, -0.17260440f);
+  q = fmaf(q, t, 0.18664083f);
+  q = fmaf(q, t, 0.024500929f);
+  q = fmaf(q, t, 0.13870965f);
+  q = fmaf(q, t, 0.13916363f);
+  q = fmaf(q, t, 0.14113952f);
+  const float tail = q * t * e;
+  return v > 0.0f ? 1.0f - tail : tail;
+}
+
 // Call f with the activation as a compile-time constant: one branch for a
 // whole row of elements (a switch an element, unrolled, cost more in branches
 // and instruction fetches than the functions themselves: the gradient
@@ -71,7 +93,10 @@ template <bool FAST, int ACT>
 __device__ __forceinline__ float act_fwd(float v) {
   if (ACT == MOE_DENSE_RELU) return v < 0.0f ? 0.0f : v;
   if (ACT == MOE_DENSE_SILU) return FAST ? __fdividef(v, 1.0f + __expf(-v)) : v / (1.0f + expf(-v));
-  if (ACT == MOE_DENSE_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (ACT == MOE_DENSE_GELU) {
+    float e;
+    return FAST ? v * normal_cdf_fast(v, e) : 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  }
   if (ACT == MOE_DENSE_GELU_TANH) return v * sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
   return v;
 }
@@ -87,10 +112,15 @@ __device__ __forceinline__ void act_both(float v, float &f, float &d) {
     f = v * s;
     d = s * (1.0f + v * (1.0f - s));
   } else if (ACT == MOE_DENSE_GELU) {
-    const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));      // normal CDF
-    const float p = 0.3989422804014327f * (FAST ? __expf(-0.5f * v * v) : expf(-0.5f * v * v));
+    float e, c;                            // e^(-v^2/2), normal distribution function
+    if (FAST) {
+      c = normal_cdf_fast(v, e);
+    } else {
+      e = expf(-0.5f * v * v);
+      c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+    }
     f = v * c;
-    d = c + v * p;
+    d = c + v * (0.3989422804014327f * e);
   } else if (ACT == MOE_DENSE_GELU_TANH) {
     const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
     f = v * s;

@@ -226,18 +226,28 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
   }
 }
 
+// 32 columns a block: warp w adds parts w, w + 8, ..., then the eight sums join
 template <typename T>
 __global__ void __launch_bounds__(256) colsum_join_kernel(const ColSums P) {
+  __shared__ float red[8][32];
   const ColSum Q = P.q[blockIdx.z];
-  const int n = blockIdx.x * 256 + threadIdx.x;
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  const int n = blockIdx.x * 32 + lane;
   pdl_wait();
   pdl_trigger();
-  if (n >= Q.N || !Q.out) return;
-  const float *p = P.part + blockIdx.z * (int64_t)P.parts * P.part_stride + n;
+  if (blockIdx.x * 32 >= Q.N || !Q.out) return;
   float v = 0.0f;
+  if (n < Q.N) {
+    const float *p = P.part + blockIdx.z * (int64_t)P.parts * P.part_stride + n;
 #pragma unroll 8
-  for (int i = 0; i < P.parts; ++i) v += p[i * P.part_stride];
-  from_f32(static_cast<T *>(Q.out)[n], v);
+    for (int i = w; i < P.parts; i += 8) v += p[i * P.part_stride];
+  }
+  red[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && n < Q.N) {
+    for (int i = 1; i < 8; ++i) v += red[i][lane];
+    from_f32(static_cast<T *>(Q.out)[n], v);
+  }
 }
 
 // enough row parts for some eight blocks an SM, at least 32 rows each
@@ -260,7 +270,7 @@ cudaError_t colsums_as(const ColSums &P, int count, int maxN, int act, bool join
     default: e = run(colsum_part_kernel<T, kNoAct>);
   }
   if (e != cudaSuccess || !join) return e;
-  return launch_kernel(colsum_join_kernel<T>, dim3((maxN + 255) / 256, 1, count), 256, 0, s, P);
+  return launch_kernel(colsum_join_kernel<T>, dim3((maxN + 31) / 32, 1, count), 256, 0, s, P);
 }
 
 unsigned grid_for(int64_t blocks, int per_sm) {

@@ -17,8 +17,8 @@
 //                                                  (= row of the tile) a thread
 //
 // A product may run over several segments of k (dx = dA W1 + dU W3) and a
-// launch over up to three products (the weight gradients), so that their last
-// waves share the GPU.  Every wait is bounded; on expiry the kernel sets the
+// launch over up to four products (dx and the weight gradients), so that they
+// share one last wave.  Every wait is bounded; on expiry the kernel sets the
 // timeout bit of the workspace's error word, lets its copies and MMAs in
 // flight finish (bounded) and returns.
 #include <algorithm>
@@ -47,7 +47,7 @@ constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kABytes = BM * BK * 2;
 constexpr int kGroupM = DT_GM;                   // row tiles of a raster group
-constexpr int kMaxProblems = 3;
+constexpr int kMaxProblems = 4;
 constexpr int kMaxSegs = 12;
 
 // A stretch of k-blocks: tensor map and plane (third coordinate) of each operand
@@ -59,6 +59,8 @@ struct TcProblem {
   CUtensorMap a[2], b[2];
   int64_t M;
   int32_t N, KB;                 // k-blocks of one segment
+  int32_t segs, amn, bmn;        // segments; A / B MN-major
+  Seg seg[kMaxSegs];
   int32_t tiles_m, tile_end;     // row tiles; tiles of this and the problems before it
   const void *bias, *bias3, *residual, *pre_in, *pre3_in;
   void *out, *pre, *pre3, *out2, *out3;
@@ -67,11 +69,19 @@ struct TcProblem {
 
 struct TcParams {
   TcProblem pr[kMaxProblems];
-  Seg seg[kMaxSegs];
-  int32_t segs, nprob, act;
+  int32_t nprob, act;
   int32_t bn, bnh;               // accumulator columns; output columns of a tile
   uint32_t *err;
 };
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 
 struct TilePos {
   int p, m, n;
@@ -94,18 +104,22 @@ __device__ __forceinline__ TilePos tile_pos(const TcParams &P, int t) {
 }
 
 // ------------------------------- epilogue pieces --------------------------------
-// 32 columns of a thread's row go through the warp's staging buffer: 16-byte
-// piece c of row r at slot c ^ f(r), free of bank conflicts both ways.
+// A warp moves its 32 rows in chunks of CW columns (64 bytes of a row: four
+// 16-byte pieces).  A thread owns a row; memory is touched by whole row
+// pieces, eight rows an instruction.  Between the two layouts lies the warp's
+// staging buffer, piece c of row r at slot c ^ (r / 2 mod 4): free of bank
+// conflicts both ways.
 template <typename T>
-__device__ __forceinline__ int stg_at(int r, int c) {
-  constexpr int PIECES = 32 * sizeof(T) / 16;
-  return r * PIECES + (PIECES == 8 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
-}
+constexpr int kCols = 64 / sizeof(T);
+constexpr int kStgBytes = 32 * 64;
+
+__device__ __forceinline__ int stg_at(int r, int c) { return r * 4 + (c ^ ((r >> 1) & 3)); }
 
 // A [M, N] matrix the epilogue reads or writes; vec: its rows are 16-byte
 // aligned, so whole pieces move at once
 template <typename T>
 struct Rows {
+  static constexpr int E = 16 / sizeof(T);
   T *p;
   int64_t ld, M;
   int N;
@@ -113,81 +127,85 @@ struct Rows {
   __device__ Rows(const void *q, int64_t ld_, int64_t M_, int N_)
       : p(static_cast<T *>(const_cast<void *>(q))), ld(ld_), M(M_), N(N_),
         vec(((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld_ * (int64_t)sizeof(T))) & 15) == 0) {}
+  __device__ __forceinline__ uint4 load(int64_t row, int col) const {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (row >= M || col >= N) return w;
+    const T *q = p + row * ld + col;
+    if (vec && col + E <= N) return *reinterpret_cast<const uint4 *>(q);
+    float v[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = col + k < N ? to_f32(q[k]) : 0.0f;
+    return pack16<T>(v);
+  }
+  __device__ __forceinline__ void store(int64_t row, int col, const uint4 &w) const {
+    if (row >= M || col >= N) return;
+    T *q = p + row * ld + col;
+    if (vec && col + E <= N) {
+      *reinterpret_cast<uint4 *>(q) = w;
+      return;
+    }
+    float v[E];
+    unpack16<T>(w, v);
+#pragma unroll
+    for (int k = 0; k < E; ++k)
+      if (col + k < N) from_f32(q[k], v[k]);
+  }
 };
 
-// v[i] of row (row0 + lane) -> column col + i
+// each thread's row, four packed pieces, to rows row0 ... of `o`
 template <typename T>
-__device__ __forceinline__ void store32(const Rows<T> &o, int64_t row0, int col, const float (&v)[32],
-                                        uint8_t *stg, int lane) {
-  constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
-  uint4 *s = reinterpret_cast<uint4 *>(stg);
+__device__ __forceinline__ void store_chunk(const Rows<T> &o, int64_t row0, int col, const uint4 (&w)[4],
+                                            uint4 *stg, int lane) {
 #pragma unroll
-  for (int c = 0; c < PIECES; ++c) s[stg_at<T>(lane, c)] = pack16<T>(v + c * E);
+  for (int c = 0; c < 4; ++c) stg[stg_at(lane, c)] = w[c];
   __syncwarp();
-  if (o.vec && col + 32 <= o.N) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int r = i * (32 / PIECES) + lane / PIECES, c = lane % PIECES;
-      if (row0 + r < o.M) *reinterpret_cast<uint4 *>(o.p + (row0 + r) * o.ld + col + c * E) = s[stg_at<T>(r, c)];
-    }
-  } else if (col < o.N) {
-    const T *e = reinterpret_cast<const T *>(stg);
-    const int rows = (int)min((int64_t)32, o.M - row0);
-    for (int r = 0; r < rows; ++r)
-      if (col + lane < o.N) o.p[(row0 + r) * o.ld + col + lane] = e[stg_at<T>(r, lane / E) * E + lane % E];
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + lane / 4, c = lane % 4;
+    o.store(row0 + r, col + c * o.E, stg[stg_at(r, c)]);
   }
   __syncwarp();
 }
 
-// The reverse in two steps: fetch reads the warp's 32 x 32 elements (zeros
-// beyond the matrix) into registers, every load instruction whole 64- or
-// 128-byte row pieces (a thread reading its own row would touch 32 lines an
-// instruction and fetch every sector twice: there is next to no L1 beside
-// the stages); get hands each thread its row through the staging buffer.
 template <typename T>
-struct Piece32 {
-  static constexpr int PIECES = 32 * sizeof(T) / 16, E = 16 / sizeof(T);
-  uint4 w[PIECES];
+__device__ __forceinline__ void store_vals(const Rows<T> &o, int64_t row0, int col, const float (&v)[kCols<T>],
+                                           uint4 *stg, int lane) {
+  uint4 w[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) w[c] = pack16<T>(v + c * o.E);
+  store_chunk(o, row0, col, w, stg, lane);
+}
+
+// a chunk on its way in: whole row pieces in registers, then staged so that
+// each thread finds its row (after a __syncwarp)
+template <typename T>
+struct Incoming {
+  uint4 w[4];
   __device__ __forceinline__ void fetch(const Rows<T> &o, int64_t row0, int col, int lane) {
-    const int c = col + lane % PIECES * E;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int64_t row = row0 + i * (32 / PIECES) + lane / PIECES;
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (row >= o.M) continue;
-      const T *p = o.p + row * o.ld + c;
-      if (o.vec && c + E <= o.N) {
-        w[i] = *reinterpret_cast<const uint4 *>(p);
-      } else {
-        float v[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) v[k] = c + k < o.N ? to_f32(p[k]) : 0.0f;
-        w[i] = pack16<T>(v);
-      }
-    }
+    for (int i = 0; i < 4; ++i) w[i] = o.load(row0 + i * 8 + lane / 4, col + lane % 4 * o.E);
   }
-  __device__ __forceinline__ void get(float (&v)[32], uint8_t *stg, int lane) const {
-    uint4 *s = reinterpret_cast<uint4 *>(stg);
+  __device__ __forceinline__ void stage(uint4 *stg, int lane) const {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) s[stg_at<T>(i * (32 / PIECES) + lane / PIECES, lane % PIECES)] = w[i];
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < PIECES; ++c) unpack16<T>(s[stg_at<T>(lane, c)], v + c * E);
-    __syncwarp();
+    for (int i = 0; i < 4; ++i) stg[stg_at(i * 8 + lane / 4, lane % 4)] = w[i];
   }
 };
 
-__device__ __forceinline__ void acc32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  tmem_ld32(taddr, r);
+// columns [taddr, taddr + N) of this thread's TMEM lane
+template <int N>
+__device__ __forceinline__ void acc_cols(uint32_t taddr, float (&v)[N]) {
+  uint32_t r[N];
+  if constexpr (N == 32) tmem_ld32(taddr, r);
+  else tmem_ld16(taddr, r);
   tmem_ld_wait();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void add_bias(float (&v)[32], const float *bias) {
+template <int N>
+__device__ __forceinline__ void add_bias(float (&v)[N], const float *bias) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < N; i += 4) {
     const float4 b = *reinterpret_cast<const float4 *>(bias + i);
     v[i] += b.x;
     v[i + 1] += b.y;
@@ -205,24 +223,28 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const float *bias) {
 template <int EPI, typename T>
 struct Epilogue {
   static constexpr bool FAST = sizeof(T) == 2;
-  static constexpr int kIn = EPI == kDenseGatedGrad ? 2 : 1;
+  static constexpr int CW = kCols<T>, E = 16 / sizeof(T);
+  static constexpr int kIn = EPI == kDenseGatedGrad ? 2 : 1;      // matrices read, staging buffers
   const TcParams &P;
   const TcProblem &Q;
   const int64_t row0;
   const int col0, c0, c1, lane;
-  uint8_t *stg;
-  Piece32<T> in[kIn];
+  uint4 *stg;
+  Incoming<T> in[kIn];
 
   __device__ Epilogue(const TcParams &p, const TcProblem &q, int64_t row, int col, int a, int b, uint8_t *st, int l)
-      : P(p), Q(q), row0(row), col0(col), c0(a), c1(min(b, q.N - col)), lane(l), stg(st) {}
+      : P(p), Q(q), row0(row), col0(col), c0(a), c1(min(b, q.N - col)), lane(l),
+        stg(reinterpret_cast<uint4 *>(st)) {}
+
+  __device__ __forceinline__ Rows<T> packed(const void *p) const { return Rows<T>(p, Q.N, Q.M, Q.N); }
 
   __device__ __forceinline__ void fetch(int c) {
     if (row0 >= Q.M || c >= c1) return;
     if (EPI == kDenseLinear && Q.residual)
       in[0].fetch(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col0 + c, lane);
     if (EPI == kDenseGatedGrad) {
-      in[0].fetch(Rows<T>(Q.pre_in, Q.N, Q.M, Q.N), row0, col0 + c, lane);
-      in[kIn - 1].fetch(Rows<T>(Q.pre3_in, Q.N, Q.M, Q.N), row0, col0 + c, lane);
+      in[0].fetch(packed(Q.pre_in), row0, col0 + c, lane);
+      in[kIn - 1].fetch(packed(Q.pre3_in), row0, col0 + c, lane);
     }
   }
   __device__ __forceinline__ void begin() { fetch(c0); }
@@ -230,69 +252,92 @@ struct Epilogue {
   __device__ __forceinline__ void run(uint32_t taddr, const float *sb) {
     if (row0 >= Q.M) return;
     const Rows<T> out(Q.out, Q.ld_o, Q.M, Q.N);
-    for (int c = c0; c < c1; c += 32) {
-      float v[32];
-      acc32(taddr + c, v);
+    for (int c = c0; c < c1; c += CW) {
+      float v[CW];
       const int col = col0 + c;
       if (EPI == kDenseStore) {
-        store32(out, row0, col, v, stg, lane);
+        acc_cols(taddr + c, v);
+        store_vals(out, row0, col, v, stg, lane);
       } else if (EPI == kDenseLinear) {
+        acc_cols(taddr + c, v);
         if (Q.bias) add_bias(v, sb + c - c0);
-        if (Q.pre) store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
+        if (Q.pre) store_vals(packed(Q.pre), row0, col, v, stg, lane);
         with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]);
+          for (int i = 0; i < CW; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]);
         });
         if (Q.residual) {
-          float r[32];
-          in[0].get(r, stg, lane);
-          fetch(c + 32);
+          in[0].stage(stg, lane);
+          __syncwarp();
+          fetch(c + CW);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] += r[i];
+          for (int k = 0; k < 4; ++k) {
+            float r[E];
+            unpack16<T>(stg[stg_at(lane, k)], r);
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[k * E + i] += r[i];
+          }
+          __syncwarp();
         }
-        store32(out, row0, col, v, stg, lane);
+        store_vals(out, row0, col, v, stg, lane);
       } else if (EPI == kDenseGated) {
-        float u[32];
-        acc32(taddr + P.bnh + c, u);
+        float u[CW];
+        acc_cols(taddr + c, v);
+        acc_cols(taddr + P.bnh + c, u);
         if (Q.bias) {
           add_bias(v, sb + c - c0);
           add_bias(u, sb + kAccCols / 4 + c - c0);
         }
         if (Q.pre) {
-          store32(Rows<T>(Q.pre, Q.N, Q.M, Q.N), row0, col, v, stg, lane);
-          store32(Rows<T>(Q.pre3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+          store_vals(packed(Q.pre), row0, col, v, stg, lane);
+          store_vals(packed(Q.pre3), row0, col, u, stg, lane);
         }
         with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]) * u[i];
+          for (int i = 0; i < CW; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]) * u[i];
         });
-        store32(out, row0, col, v, stg, lane);
+        store_vals(out, row0, col, v, stg, lane);
       } else {                                           // kDenseGatedGrad
-        float a[32], u[32];
-        in[0].get(a, stg, lane);
-        in[kIn - 1].get(u, stg, lane);
-        fetch(c + 32);
+        // a and u staged side by side; dA, dU and h packed piece by piece, so
+        // that no more than one matrix is held in fp32
+        uint4 *stg_u = stg + (kIn - 1) * (kStgBytes / 16);
+        in[0].stage(stg, lane);
+        in[kIn - 1].stage(stg_u, lane);
+        __syncwarp();
+        fetch(c + CW);
+        acc_cols(taddr + c, v);
+        uint4 da[4], du[4], hh[4];
         with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float f, d;
-            act_both<FAST, decltype(A)::value>(a[i], f, d);
-            const float dh = v[i];
-            v[i] = dh * u[i] * d;
-            a[i] = dh * f;
-            u[i] = f * u[i];
+          for (int k = 0; k < 4; ++k) {
+            float a[E], u[E], h[E];
+            unpack16<T>(stg[stg_at(lane, k)], a);
+            unpack16<T>(stg_u[stg_at(lane, k)], u);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              float f, d;
+              act_both<FAST, decltype(A)::value>(a[i], f, d);
+              const float dh = v[k * E + i];
+              a[i] = dh * u[i] * d;
+              h[i] = f * u[i];
+              u[i] = dh * f;
+            }
+            da[k] = pack16<T>(a);
+            du[k] = pack16<T>(u);
+            hh[k] = pack16<T>(h);
           }
         });
-        store32(out, row0, col, v, stg, lane);
-        store32(Rows<T>(Q.out2, Q.N, Q.M, Q.N), row0, col, a, stg, lane);
-        store32(Rows<T>(Q.out3, Q.N, Q.M, Q.N), row0, col, u, stg, lane);
+        __syncwarp();
+        store_chunk(out, row0, col, da, stg, lane);
+        store_chunk(packed(Q.out2), row0, col, du, stg_u, lane);
+        store_chunk(packed(Q.out3), row0, col, hh, stg, lane);
       }
     }
   }
 };
 
 // --------------------------------- the kernel ----------------------------------
-template <int EPI, bool AMN, bool BMN, typename T>
+template <int EPI, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dense_pair_kernel(const __grid_constant__ TcParams P) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -356,8 +401,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int am = q.m * 2 * BM + (int)rank * BM;
       // gated: the even CTA stages rows of W1, the odd one the same rows of W3
       const int bn0 = q.n * P.bnh + (EPI == kDenseGated ? 0 : (int)rank * (P.bn / 2));
-      for (int sg = 0; ok && sg < P.segs; ++sg) {
-        const Seg S = P.seg[sg];
+      for (int sg = 0; ok && sg < Q.segs; ++sg) {
+        const Seg S = Q.seg[sg];
         const CUtensorMap *ma = &Q.a[S.a];
         const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
         for (int kb = 0; kb < Q.KB; kb += kBks) {
@@ -373,13 +418,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           for (int q2 = 0; q2 < nq; ++q2) {
             const int k = (kb + q2) * BK;
-            if (AMN) {
+            if (Q.amn) {
               tma_load_3d_pair(sa, ma, fb, am, k, S.az);
               tma_load_3d_pair(sa + 8192, ma, fb, am + 64, k, S.az);
             } else {
               tma_load_3d_pair(sa, ma, fb, k, am, S.az);
             }
-            if (BMN) {
+            if (Q.bmn) {
               tma_load_3d_pair(sb, mb, fb, bn0, k, S.bz);
               if (P.bn == 256) tma_load_3d_pair(sb + 8192, mb, fb, bn0 + 64, k, S.bz);
             } else {
@@ -398,17 +443,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------ MMA issuer (even CTA only) ------------------------
-    const uint32_t idesc = idesc_bf16(2 * BM, P.bn) | (AMN ? 1u << 15 : 0u) | (BMN ? 1u << 16 : 0u);
+    // (K-major: a K step of 16 is 32 bytes on; MN-major: 16 lines of 128 bytes)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += npairs) {
-      const int KB = P.pr[tile_pos(P, t).p].KB;
+      const TcProblem &Q = P.pr[tile_pos(P, t).p];
+      const int KB = Q.KB, segs = Q.segs;
+      const bool amn = Q.amn, bmn = Q.bmn;
+      const uint32_t idesc = idesc_bf16(2 * BM, P.bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
       if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
       uint32_t accum = 0;
-      for (int sg = 0; ok && sg < P.segs; ++sg) {
+      for (int sg = 0; ok && sg < segs; ++sg) {
         for (int kb = 0; kb < KB; kb += kBks) {
           if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
           tc_fence_after();
@@ -418,8 +466,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t a_addr = a0 + q2 * kABytes, b_addr = a0 + kBks * kABytes + q2 * b_bytes;
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
-              umma_bf16_pair(d_tmem, AMN ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
-                             BMN ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc, accum);
+              umma_bf16_pair(d_tmem, amn ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
+                             bmn ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc, accum);
               accum = 1;
             }
           }
@@ -438,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // two warps a TMEM lane quarter (a warp reaches lanes 32 (warp mod 4) ...
     // of its CTA only), each with half of the tile's columns
     const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
-    uint8_t *stg = smem + (size_t)kStages * stage_bytes + (size_t)ew * (32 * 32 * sizeof(T));
+    uint8_t *stg = smem + (size_t)kStages * stage_bytes + (size_t)ew * (Epilogue<EPI, T>::kIn * kStgBytes);
     const uint32_t acce_even[2] = {mapa_shared(smem_u32(&acce_bar[0]), 0), mapa_shared(smem_u32(&acce_bar[1]), 0)};
     float *sb = s_bias[ew];
     int acc = 0;
@@ -506,19 +554,15 @@ cudaError_t pairs_of(size_t smem, int *pairs) {
   return cudaSuccess;
 }
 
-template <typename T>
-constexpr size_t smem_bytes() {
-  return 1024 + kStages * kBks * (kABytes + 128 * BK * 2) + kEpiWarps * 32 * 32 * sizeof(T);
-}
-
-template <int EPI, bool AMN, bool BMN, typename T>
+template <int EPI, typename T>
 cudaError_t launch_pair_as(const TcParams &P, cudaStream_t s) {
-  constexpr auto kern = dense_pair_kernel<EPI, AMN, BMN, T>;
+  constexpr auto kern = dense_pair_kernel<EPI, T>;
+  constexpr size_t smem = 1024 + kStages * kBks * (kABytes + 128 * BK * 2) +
+                          kEpiWarps * Epilogue<EPI, T>::kIn * kStgBytes;
   int pairs = 0;
-  const cudaError_t e = pairs_of<kern>(smem_bytes<T>(), &pairs);
+  const cudaError_t e = pairs_of<kern>(smem, &pairs);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, 2 * (unsigned)std::min<int>(pairs, P.pr[P.nprob - 1].tile_end), kThreads,
-                       smem_bytes<T>(), s, P);
+  return launch_kernel(kern, 2 * (unsigned)std::min<int>(pairs, P.pr[P.nprob - 1].tile_end), kThreads, smem, s, P);
 }
 
 bool kmajor(const Operand &o) { return o.ks == 1; }
@@ -549,11 +593,8 @@ bool dense_tc_ok(const DenseGemm &g) {
     if (o->p && !tma_ok(*o, g.N, g.K)) return false;
   for (const Operand *o : {&g.a, &g.a2})
     if (o->p && !tma_ok(*o, g.M, g.K)) return false;
-  const bool am = !kmajor(g.a), bm = !kmajor(g.b);
-  if (g.a2.p && (am != !kmajor(g.a2) || bm != !kmajor(g.b2))) return false;
-  if (g.epi == kDenseLinear || g.epi == kDenseGated) return !am && !bm && (!g.b3.p || kmajor(g.b3));
-  if (g.epi == kDenseGatedGrad) return !am && bm;
-  return bm;
+  return (!g.a2.p || (kmajor(g.a) == kmajor(g.a2) && kmajor(g.b) == kmajor(g.b2))) &&
+         (!g.b3.p || kmajor(g.b) == kmajor(g.b3)) && (g.epi != kDenseGated || kmajor(g.b));
 }
 
 cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s) {
@@ -562,28 +603,32 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
   P.err = err;
   P.act = g[0].act;
   P.nprob = n;
-  P.segs = g[0].a2.p ? 2 : 1;
-  for (int i = 0; i < P.segs; ++i) P.seg[i] = {(uint8_t)i, 0, (uint8_t)i, 0};
   // columns of a tile: the width whose last wave wastes less (a 128-column
   // tile costs about 0.55 of a 256-column one)
   const bool gated = g[0].epi == kDenseGated;
   const int pairs = std::max(1, device_sms() / 2);
-  auto tiles_at = [&](int bn, int upto) {
+  auto tiles_of = [&](const DenseGemm &q, int bn) {
+    const int w = gated ? bn / 2 : bn;
+    return ((q.M + 2 * BM - 1) / (2 * BM)) * ((q.N + w - 1) / w);
+  };
+  auto tiles_at = [&](int bn) {
     int64_t t = 0;
-    for (int p = 0; p < upto; ++p) {
-      const int w = gated ? bn / 2 : bn;
-      t += ((g[p].M + 2 * BM - 1) / (2 * BM)) * ((g[p].N + w - 1) / w);
-    }
+    for (int p = 0; p < n; ++p) t += tiles_of(g[p], bn);
     return t;
   };
-  auto cost = [&](int bn) { return (double)((tiles_at(bn, n) + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55); };
+  auto cost = [&](int bn) { return (double)((tiles_at(bn) + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55); };
   P.bn = cost(128) < cost(256) ? 128 : 256;
   P.bnh = gated ? P.bn / 2 : P.bn;
-  if (tiles_at(P.bn, n) > 0x3fffffff) return cudaErrorInvalidValue;
+  if (tiles_at(P.bn) > 0x3fffffff) return cudaErrorInvalidValue;
   auto box_b = [&](const Operand &o) { return kmajor(o) ? P.bn / 2 : BK; };
+  // longest contractions first: the last wave is then one of short tiles
+  int order[kMaxProblems] = {0, 1, 2, 3};
+  auto depth = [&](int p) { return g[p].K * (g[p].a2.p ? 2 : 1); };
+  std::stable_sort(order, order + n, [&](int a, int b) { return depth(a) > depth(b); });
+  int64_t end = 0;
   for (int p = 0; p < n; ++p) {
     TcProblem &Q = P.pr[p];
-    const DenseGemm &G = g[p];
+    const DenseGemm &G = g[order[p]];
     bool ok = map_operand(&Q.a[0], G.a, G.M, G.K, kmajor(G.a) ? BM : BK, 1, 0) &&
               map_operand(&Q.b[0], G.b, G.N, G.K, box_b(G.b), 1, 0);
     if (G.a2.p)
@@ -591,11 +636,15 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
            map_operand(&Q.b[1], G.b2, G.N, G.K, box_b(G.b2), 1, 0);
     if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, box_b(G.b3), 1, 0);
     if (!ok) return cudaErrorInvalidValue;
+    Q.segs = G.a2.p ? 2 : 1;
+    for (int i = 0; i < Q.segs; ++i) Q.seg[i] = {(uint8_t)i, 0, (uint8_t)i, 0};
+    Q.amn = !kmajor(G.a);
+    Q.bmn = !kmajor(G.b);
     Q.M = G.M;
     Q.N = G.N;
     Q.KB = (int32_t)((G.K + BK - 1) / BK);
     Q.tiles_m = (int32_t)((G.M + 2 * BM - 1) / (2 * BM));
-    Q.tile_end = (int32_t)tiles_at(P.bn, p + 1);
+    Q.tile_end = (int32_t)(end += tiles_of(G, P.bn));
     Q.bias = G.bias;
     Q.bias3 = G.bias3;
     Q.residual = G.residual;
@@ -611,12 +660,10 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
   }
   using B = __nv_bfloat16;
   switch (g[0].epi) {
-    case kDenseLinear: return launch_pair_as<kDenseLinear, false, false, B>(P, s);
-    case kDenseGated: return launch_pair_as<kDenseGated, false, false, B>(P, s);
-    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, false, true, B>(P, s);
-    default:
-      return kmajor(g[0].a) ? launch_pair_as<kDenseStore, false, true, B>(P, s)
-                            : launch_pair_as<kDenseStore, true, true, B>(P, s);
+    case kDenseLinear: return launch_pair_as<kDenseLinear, B>(P, s);
+    case kDenseGated: return launch_pair_as<kDenseGated, B>(P, s);
+    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, B>(P, s);
+    default: return launch_pair_as<kDenseStore, B>(P, s);
   }
 }
 
