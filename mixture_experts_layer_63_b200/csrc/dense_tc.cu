@@ -43,6 +43,7 @@ constexpr int kBks = DT_BKS;                 // k-blocks of a stage
 constexpr int kStages = 6 / kBks;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kRegsLaunch = 168, kRegsLow = 56, kRegsHigh = 224;
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kABytes = BM * BK * 2;
@@ -81,6 +82,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+// tma_load_3d_pair to a shared-memory address
+__device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                               int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
 }
 
 struct TilePos {
@@ -127,6 +138,11 @@ struct Rows {
   __device__ Rows(const void *q, int64_t ld_, int64_t M_, int N_)
       : p(static_cast<T *>(const_cast<void *>(q))), ld(ld_), M(M_), N(N_),
         vec(((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld_ * (int64_t)sizeof(T))) & 15) == 0) {}
+  // the warp's chunk lies inside and moves in whole pieces: one branch a
+  // chunk (a branch a piece serialises the accesses)
+  __device__ __forceinline__ bool whole(int64_t row0, int col) const {
+    return vec && row0 + 32 <= M && col + kCols<T> <= N;
+  }
   __device__ __forceinline__ uint4 load(int64_t row, int col) const {
     uint4 w = make_uint4(0, 0, 0, 0);
     if (row >= M || col >= N) return w;
@@ -159,10 +175,16 @@ __device__ __forceinline__ void store_chunk(const Rows<T> &o, int64_t row0, int 
 #pragma unroll
   for (int c = 0; c < 4; ++c) stg[stg_at(lane, c)] = w[c];
   __syncwarp();
+  const int r0 = lane / 4, c = lane % 4;
+  if (o.whole(row0, col)) {
+    uint4 v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + lane / 4, c = lane % 4;
-    o.store(row0 + r, col + c * o.E, stg[stg_at(r, c)]);
+    for (int i = 0; i < 4; ++i) v[i] = stg[stg_at(i * 8 + r0, c)];
+    T *q = o.p + (row0 + r0) * o.ld + col + c * o.E;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(q + i * 8 * o.ld) = v[i];
+  } else {
+    for (int i = 0; i < 4; ++i) o.store(row0 + i * 8 + r0, col + c * o.E, stg[stg_at(i * 8 + r0, c)]);
   }
   __syncwarp();
 }
@@ -182,8 +204,14 @@ template <typename T>
 struct Incoming {
   uint4 w[4];
   __device__ __forceinline__ void fetch(const Rows<T> &o, int64_t row0, int col, int lane) {
+    if (o.whole(row0, col)) {
+      const T *q = o.p + (row0 + lane / 4) * o.ld + col + lane % 4 * o.E;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = o.load(row0 + i * 8 + lane / 4, col + lane % 4 * o.E);
+      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(q + i * 8 * o.ld);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = o.load(row0 + i * 8 + lane / 4, col + lane % 4 * o.E);
+    }
   }
   __device__ __forceinline__ void stage(uint4 *stg, int lane) const {
 #pragma unroll
@@ -390,10 +418,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = s_tmem_base;
   const uint64_t s_limit = s_limit_sh;
 
+  // Registers: 168 a thread at launch (384 threads); the four warps of the
+  // first warpgroup give most of theirs to the epilogue:
+  // 128 * 56 + 256 * 224 = 384 * 168
+  static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "registers of the block");
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
   if (warp == 0 && lane == 0) {
     // ------------------------------ TMA producer ------------------------------
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
+    const uint32_t smem0 = smem_u32(smem), fb0 = smem_u32(full_bar) & 0xFEFFFFFFu;      // the even CTA's barriers
+    const bool wide = P.bn == 256;
+    // k-blocks [0, KB) of one segment; the operand orders are constants of the
+    // loop (a stage has to be refilled within the time of one stage's MMAs)
+    auto fill = [&](auto amn, auto bmn, const CUtensorMap *ma, const CUtensorMap *mb, int am, int bn0, int KB,
+                    Seg S) -> bool {
+      for (int kb = 0; kb < KB; kb += kBks) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) return false;
+        uint32_t sa = smem0 + (uint32_t)stage * stage_bytes, sb = sa + kBks * kABytes;
+        const uint32_t fb = fb0 + 8 * stage;
+        const int nq = min(kBks, KB - kb);
+        if (rank == 0) {
+          mbar_expect_tx(&full_bar[stage], 2 * nq * (kABytes + b_bytes));
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        }
+#pragma unroll
+        for (int q2 = 0; q2 < kBks; ++q2) {
+          if (q2 >= nq) break;
+          const int k = (kb + q2) * BK;
+          if (decltype(amn)::value) {
+            tma_load_3d_at(sa, ma, fb, am, k, S.az);
+            tma_load_3d_at(sa + 8192, ma, fb, am + 64, k, S.az);
+          } else {
+            tma_load_3d_at(sa, ma, fb, k, am, S.az);
+          }
+          if (decltype(bmn)::value) {
+            tma_load_3d_at(sb, mb, fb, bn0, k, S.bz);
+            if (wide) tma_load_3d_at(sb + 8192, mb, fb, bn0 + 64, k, S.bz);
+          } else {
+            tma_load_3d_at(sb, mb, fb, k, bn0, S.bz);
+          }
+          sa += kABytes;
+          sb += b_bytes;
+        }
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      }
+      return true;
+    };
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += npairs) {
       const TilePos q = tile_pos(P, t);
@@ -405,35 +478,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Seg S = Q.seg[sg];
         const CUtensorMap *ma = &Q.a[S.a];
         const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
-        for (int kb = 0; kb < Q.KB; kb += kBks) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) { ok = false; break; }
-          uint8_t *sa = smem + (size_t)stage * stage_bytes;
-          uint8_t *sb = sa + kBks * kABytes;
-          const uint32_t fb = smem_u32(&full_bar[stage]) & 0xFEFFFFFFu;      // the even CTA's barrier
-          const int nq = min(kBks, Q.KB - kb);
-          if (rank == 0) {
-            mbar_expect_tx(&full_bar[stage], 2 * nq * (kABytes + b_bytes));
-            armed |= 1u << stage;
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          }
-          for (int q2 = 0; q2 < nq; ++q2) {
-            const int k = (kb + q2) * BK;
-            if (Q.amn) {
-              tma_load_3d_pair(sa, ma, fb, am, k, S.az);
-              tma_load_3d_pair(sa + 8192, ma, fb, am + 64, k, S.az);
-            } else {
-              tma_load_3d_pair(sa, ma, fb, k, am, S.az);
-            }
-            if (Q.bmn) {
-              tma_load_3d_pair(sb, mb, fb, bn0, k, S.bz);
-              if (P.bn == 256) tma_load_3d_pair(sb + 8192, mb, fb, bn0 + 64, k, S.bz);
-            } else {
-              tma_load_3d_pair(sb, mb, fb, k, bn0, S.bz);
-            }
-            sa += kABytes;
-            sb += b_bytes;
-          }
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        if (Q.amn) {
+          ok = Q.bmn ? fill(IntC<1>{}, IntC<1>{}, ma, mb, am, bn0, Q.KB, S)
+                     : fill(IntC<1>{}, IntC<0>{}, ma, mb, am, bn0, Q.KB, S);
+        } else {
+          ok = Q.bmn ? fill(IntC<0>{}, IntC<1>{}, ma, mb, am, bn0, Q.KB, S)
+                     : fill(IntC<0>{}, IntC<0>{}, ma, mb, am, bn0, Q.KB, S);
         }
       }
     }
@@ -444,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------ MMA issuer (even CTA only) ------------------------
     // (K-major: a K step of 16 is 32 bytes on; MN-major: 16 lines of 128 bytes)
+    const uint32_t smem0 = smem_u32(smem);
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
@@ -452,6 +503,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int KB = Q.KB, segs = Q.segs;
       const bool amn = Q.amn, bmn = Q.bmn;
       const uint32_t idesc = idesc_bf16(2 * BM, P.bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
+      // descriptors of stage 0; the address field counts 16 bytes
+      const uint64_t adesc = amn ? mn128_desc(smem0) : sw128_desc(smem0);
+      const uint64_t bdesc = bmn ? mn128_desc(smem0 + kBks * kABytes) : sw128_desc(smem0 + kBks * kABytes);
+      const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
       if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
@@ -460,16 +515,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int kb = 0; kb < KB; kb += kBks) {
           if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + (size_t)stage * stage_bytes);
+          uint64_t ad = adesc + (uint32_t)stage * (stage_bytes >> 4), bd = bdesc + (uint32_t)stage * (stage_bytes >> 4);
           const int nq = min(kBks, KB - kb);
           for (int q2 = 0; q2 < nq; ++q2) {
-            const uint32_t a_addr = a0 + q2 * kABytes, b_addr = a0 + kBks * kABytes + q2 * b_bytes;
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
-              umma_bf16_pair(d_tmem, amn ? mn128_desc(a_addr + k * 2048) : sw128_desc(a_addr + k * 32),
-                             bmn ? mn128_desc(b_addr + k * 2048) : sw128_desc(b_addr + k * 32), idesc, accum);
+              umma_bf16_pair(d_tmem, ad + k * astep, bd + k * bstep, idesc, accum);
               accum = 1;
             }
+            ad += kABytes >> 4;
+            bd += b_bytes >> 4;
           }
           umma_commit_pair_both(&empty_bar[stage]);
           if (++stage == kStages) { stage = 0; phase ^= 1u; }
@@ -481,8 +536,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     umma_commit_pair_local(&drain_bar);
     mbar_wait_drain(&drain_bar, 0);
-  } else if (warp >= 4) {
+  }
+  __syncwarp();
+  } else {
     // -------------------------------- epilogue --------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
     // two warps a TMEM lane quarter (a warp reaches lanes 32 (warp mod 4) ...
     // of its CTA only), each with half of the tile's columns
     const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
@@ -537,6 +595,11 @@ cudaError_t pairs_of(size_t smem, int *pairs) {
   if (e != cudaSuccess) return e;
   int n = dev < kMaxDevices ? cache[dev].load(std::memory_order_acquire) : 0;
   if (n == 0) {
+    // the epilogue's larger share must be there: it would wait for it forever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
