@@ -118,6 +118,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
 
 // n products of one kind: on the tensor cores where all of them fit there
 cudaError_t run_products(const DenseGemm *g, int n, char *ws, cudaStream_t s) {
+  if (n == 1 && dense_few_ok(g[0])) return launch_dense_few(g[0], reinterpret_cast<uint32_t *>(ws), s);
   bool tc = true;
   for (int i = 0; i < n; ++i) tc = tc && dense_tc_ok(g[i]);
   if (tc) return launch_dense_tc(g, n, reinterpret_cast<uint32_t *>(ws), s);

@@ -1,0 +1,297 @@
+// The dense operators' forward products for few rows (decoding, small
+// batches): the time is the stream of the weights.
+//
+//   out[t, n] = epilogue(sum_k x(t, k) W(n, k)),  bf16, both K-major
+//
+// The weights take the MMA's M side (128 rows of W a CTA) and the tokens its
+// N side (a multiple of 16), so one token costs no more than the weights'
+// bytes.  To keep enough bytes in flight on all SMs the contraction is split
+// over a cluster of up to eight CTAs: each streams its share of k through a
+// TMA ring, leaves its fp32 partial tile in its shared memory, and the CTAs of
+// the cluster then add the tokens among them in rank order, reading one
+// another's partials (distributed shared memory).  No atomics and no second
+// pass over global memory: the same bits on every call.  The gated block
+// streams W1 and W3 side by side into two accumulators.
+//
+//   warp 0  TMA producer, warp 1  MMA issuer, all four warps  epilogue
+#include <algorithm>
+#include <atomic>
+
+#include "dense_internal.h"
+#include "dense_math.cuh"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BN = 128;                 // rows of W a CTA (the MMA's M)
+constexpr int BK = 64;
+constexpr int kThreads = 128;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kWBytes = BN * BK * 2;
+
+struct FewParams {
+  CUtensorMap x, w, w3;
+  int64_t M;
+  int32_t N, KB;                 // k-blocks in all
+  int32_t tt;                    // tokens of a tile (the MMA's N)
+  int32_t stages, split, tmem_cols, act;
+  const void *bias, *bias3, *residual;
+  void *out, *pre, *pre3;
+  int64_t ld_r, ld_o;
+  uint32_t *err;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
+                                            int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_constant__ FewParams P) {
+  using T = __nv_bfloat16;
+  constexpr int NW = GATED ? 2 : 1;                // weight tiles of a stage
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t empty_bar[kMaxStages];
+  __shared__ __align__(8) uint64_t acc_bar;
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  __shared__ uint64_t s_limit_sh;
+
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t x_bytes = (uint32_t)P.tt * BK * 2, stage_bytes = NW * kWBytes + x_bytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = P.split, rank = (int)(blockIdx.x % (unsigned)split);
+  const int n0 = (int)(blockIdx.x / (unsigned)split) * BN;
+  const int64_t t0 = (int64_t)blockIdx.y * P.tt;
+  const int kb0 = (int)((int64_t)P.KB * rank / split), kb1 = (int)((int64_t)P.KB * (rank + 1) / split);
+
+  if (tid == 32) {
+    for (int i = 0; i < P.stages; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    mbar_init(&acc_bar, 1);
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem_base)),
+                 "r"(P.tmem_cols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    tma_prefetch_map(&P.x);
+    tma_prefetch_map(&P.w);
+    if (GATED) tma_prefetch_map(&P.w3);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) s_limit_sh = wait_limit_ns(P.err);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem_base;
+  const uint64_t s_limit = s_limit_sh;
+  const uint32_t smem0 = smem_u32(smem);
+
+  if (warp == 0 && lane == 0) {
+    int stage = 0, kb = kb0;
+    uint32_t phase = 0;
+    for (; kb < kb1; ++kb) {
+      if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) break;
+      const uint32_t s0 = smem0 + (uint32_t)stage * stage_bytes, fb = smem_u32(&full_bar[stage]);
+      mbar_expect_tx(&full_bar[stage], stage_bytes);
+      tma_load_3d(s0, &P.w, fb, kb * BK, n0, 0);
+      if (GATED) tma_load_3d(s0 + kWBytes, &P.w3, fb, kb * BK, n0, 0);
+      tma_load_3d(s0 + NW * kWBytes, &P.x, fb, kb * BK, (int)t0, 0);
+      if (++stage == P.stages) { stage = 0; phase ^= 1u; }
+    }
+    // aborting: the last round of each stage has to land before the exit
+    if (kb < kb1)
+      for (int i = kb - 1, n = 0; i >= kb0 && n < P.stages; --i, ++n)
+        mbar_wait_drain(&full_bar[(i - kb0) % P.stages], (uint32_t)((i - kb0) / P.stages) & 1u);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(BN, P.tt);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(&full_bar[stage], phase, &s_abort, P.err, s_limit)) break;
+      tc_fence_after();
+      const uint32_t s0 = smem0 + (uint32_t)stage * stage_bytes;
+      const uint64_t wd = sw128_desc(s0), xd = sw128_desc(s0 + NW * kWBytes);
+#pragma unroll
+      for (int k = 0; k < BK / 16; ++k) {
+        const uint32_t on = kb > kb0 || k > 0 ? 1u : 0u;
+        umma_bf16(tmem_base, wd + 2 * k, xd + 2 * k, idesc, on);
+        if (GATED) umma_bf16(tmem_base + P.tt, wd + (kWBytes >> 4) + 2 * k, xd + 2 * k, idesc, on);
+      }
+      umma_commit(&empty_bar[stage]);
+      if (++stage == P.stages) { stage = 0; phase ^= 1u; }
+    }
+    umma_commit(&acc_bar);
+    umma_commit(&drain_bar);
+    mbar_wait_drain(&drain_bar, 0);
+  }
+  __syncwarp();
+
+  // the partial tile, [matrix][token][row of W] fp32, over the stages (all of
+  // them have been read: the accumulator is complete)
+  const bool done = __syncthreads_and(mbar_wait(&acc_bar, 0, &s_abort, P.err, s_limit)) && !s_abort;
+  tc_fence_after();
+  float *part = reinterpret_cast<float *>(smem);
+  if (done) {
+    const uint32_t ta = tmem_base + ((uint32_t)(warp * 32) << 16);
+    for (int c = 0; c < NW * P.tt; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(ta + c, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) part[(c + i) * BN + tid] = kb1 > kb0 ? __uint_as_float(r[i]) : 0.0f;
+    }
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  if (done) {
+    // tokens rank, rank + split, ...: thread = row of W
+    const int n = n0 + tid;
+    const bool in = n < P.N;
+    const float b = in && P.bias ? to_f32(static_cast<const T *>(P.bias)[n]) : 0.0f;
+    const float b3 = GATED && in && P.bias3 ? to_f32(static_cast<const T *>(P.bias3)[n]) : 0.0f;
+    const int nt = (int)min((int64_t)P.tt, P.M - t0);
+    const uint32_t p0 = smem0 + 4u * tid;
+    for (int t = rank; t < nt; t += split) {
+      float v = 0.0f, u = 0.0f;
+      for (int r = 0; r < split; ++r) {
+        const uint32_t p = mapa_shared(p0 + (uint32_t)t * BN * 4, (uint32_t)r);
+        v += ld_cluster_f32(p);
+        if (GATED) u += ld_cluster_f32(p + (uint32_t)P.tt * BN * 4);
+      }
+      if (!in) continue;
+      const int64_t m = t0 + t;
+      v += b;
+      if (P.pre) from_f32(static_cast<T *>(P.pre)[m * P.N + n], v);
+      with_act(P.act, [&](auto A) { v = act_fwd<true, decltype(A)::value>(v); });
+      if (GATED) {
+        u += b3;
+        if (P.pre3) from_f32(static_cast<T *>(P.pre3)[m * P.N + n], u);
+        v *= u;
+      } else if (P.residual) {
+        v += to_f32(static_cast<const T *>(P.residual)[m * P.ld_r + n]);
+      }
+      from_f32(static_cast<T *>(P.out)[m * P.ld_o + n], v);
+    }
+  }
+  cluster_sync_all();              // no CTA leaves while another may read its partial tile
+  tc_fence_after();
+  if (warp == 2)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(P.tmem_cols));
+}
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kMaxSmem = 220 * 1024;
+
+template <auto kern>
+cudaError_t allow_smem() {
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < kMaxDevices && done[dev].load(std::memory_order_acquire))) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+template <bool GATED>
+cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, size_t smem, cudaStream_t s) {
+  constexpr auto kern = dense_few_kernel<GATED>;
+  cudaError_t e = allow_smem<kern>();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * (unsigned)P.split, ttiles);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)P.split, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = MOE_PDL ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, P);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace
+
+// Tokens up to which this kernel takes a forward product
+bool dense_few_ok(const DenseGemm &g) {
+  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.M <= 128 && dense_tc_ok(g);
+}
+
+cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {
+  const bool gated = g.epi == kDenseGated;
+  const int nw = gated ? 2 : 1;
+  FewParams P{};
+  P.tt = (int)std::min<int64_t>(128, (g.M + 15) / 16 * 16);
+  const size_t stage = (size_t)nw * kWBytes + (size_t)P.tt * BK * 2;
+  // two CTAs an SM where that leaves each at least three stages
+  const size_t half = 108 * 1024;
+  const bool two = 3 * stage <= half;
+  P.stages = (int)std::min<size_t>(kMaxStages, (two ? half : kMaxSmem - 1024) / stage);
+  P.KB = (int)((g.K + BK - 1) / BK);
+  const int64_t tiles = (g.N + BN - 1) / BN, ttiles = (g.M + P.tt - 1) / P.tt;
+  const int64_t room = (int64_t)device_sms() * (two ? 2 : 1);
+  P.split = 1;
+  while (P.split < 8 && tiles * ttiles * P.split * 2 <= room && P.KB / (P.split * 2) >= 2) P.split *= 2;
+  P.tmem_cols = 32;
+  while (P.tmem_cols < nw * P.tt) P.tmem_cols *= 2;
+  const size_t smem = 1024 + std::max(P.stages * stage, (size_t)nw * P.tt * BN * 4);
+  if (!make_map3d(&P.x, g.a.p, g.K, g.M, 1, g.M == 1 ? (g.K + 7) / 8 * 8 : g.a.rs,
+                  (g.M == 1 ? (g.K + 7) / 8 * 8 : g.a.rs) * g.M, P.tt) ||
+      !make_map3d(&P.w, g.b.p, g.K, g.N, 1, g.N == 1 ? (g.K + 7) / 8 * 8 : g.b.rs,
+                  (g.N == 1 ? (g.K + 7) / 8 * 8 : g.b.rs) * g.N, BN) ||
+      (gated && !make_map3d(&P.w3, g.b3.p, g.K, g.N, 1, g.N == 1 ? (g.K + 7) / 8 * 8 : g.b3.rs,
+                            (g.N == 1 ? (g.K + 7) / 8 * 8 : g.b3.rs) * g.N, BN)))
+    return cudaErrorInvalidValue;
+  P.M = g.M;
+  P.N = g.N;
+  P.act = g.act;
+  P.bias = g.bias;
+  P.bias3 = g.bias3;
+  P.residual = g.residual;
+  P.out = g.out;
+  P.pre = g.pre;
+  P.pre3 = g.pre3;
+  P.ld_r = g.ld_r;
+  P.ld_o = g.ld_o;
+  P.err = err;
+  return gated ? launch_few_as<true>(P, (unsigned)tiles, (unsigned)ttiles, smem, s)
+               : launch_few_as<false>(P, (unsigned)tiles, (unsigned)ttiles, smem, s);
+}
+
+}  // namespace moe

@@ -53,6 +53,10 @@ cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 bool dense_tc_ok(const DenseGemm &g);
 cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
 
+// Forward products of few rows (dense_few.cu)
+bool dense_few_ok(const DenseGemm &g);
+cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s);
+
 // Column sums out[n] = sum_m src[m, n] (fp32, in a fixed order), up to three
 // matrices of M rows in one launch.  With z and dz (packed [M, N]):
 // dz = src * act'(z) first, and the sums are dz's; out may then be null.
