@@ -13,7 +13,7 @@
 // pass over global memory: the same bits on every call.  The gated block
 // streams W1 and W3 side by side into two accumulators.
 //
-//   warp 0  TMA producer, warp 1  MMA issuer, all four warps  epilogue
+//   warp 0  TMA producer, warp 1  MMA issuer, all eight warps  epilogue
 #include <algorithm>
 #include <atomic>
 
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int BN = 128;                 // rows of W a CTA (the MMA's M)
 constexpr int BK = 64;
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kWBytes = BN * BK * 2;
 
@@ -62,7 +62,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
 
@@ -162,46 +162,73 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
   const bool done = __syncthreads_and(mbar_wait(&acc_bar, 0, &s_abort, P.err, s_limit)) && !s_abort;
   tc_fence_after();
   float *part = reinterpret_cast<float *>(smem);
+  const int row = tid % BN;                        // of W
   if (done) {
-    const uint32_t ta = tmem_base + ((uint32_t)(warp * 32) << 16);
-    for (int c = 0; c < NW * P.tt; c += 16) {
+    // (a warp reaches TMEM lanes 32 (warp mod 4) ...; its half of the columns)
+    const uint32_t ta = tmem_base + ((uint32_t)((warp & 3) * 32) << 16);
+    for (int c = 16 * (warp >> 2); c < NW * P.tt; c += 32) {
       uint32_t r[16];
       tmem_ld16(ta + c, r);
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c + i) * BN + tid] = kb1 > kb0 ? __uint_as_float(r[i]) : 0.0f;
+      for (int i = 0; i < 16; ++i) part[(c + i) * BN + row] = kb1 > kb0 ? __uint_as_float(r[i]) : 0.0f;
     }
   }
   tc_fence_before();
   cluster_sync_all();
   if (done) {
-    // tokens rank, rank + split, ...: thread = row of W
-    const int n = n0 + tid;
+    // tokens by rank, two thread halves within a rank
+    const int n = n0 + row, step = 2 * split;
     const bool in = n < P.N;
     const float b = in && P.bias ? to_f32(static_cast<const T *>(P.bias)[n]) : 0.0f;
     const float b3 = GATED && in && P.bias3 ? to_f32(static_cast<const T *>(P.bias3)[n]) : 0.0f;
     const int nt = (int)min((int64_t)P.tt, P.M - t0);
-    const uint32_t p0 = smem0 + 4u * tid;
-    for (int t = rank; t < nt; t += split) {
-      float v = 0.0f, u = 0.0f;
-      for (int r = 0; r < split; ++r) {
-        const uint32_t p = mapa_shared(p0 + (uint32_t)t * BN * 4, (uint32_t)r);
-        v += ld_cluster_f32(p);
-        if (GATED) u += ld_cluster_f32(p + (uint32_t)P.tt * BN * 4);
+    const uint32_t p0 = smem0 + 4u * row, m3 = (uint32_t)P.tt * BN * 4;
+    // U tokens at a time, the partials of four ranks in flight for each,
+    // added in rank order
+    constexpr int U = GATED ? 2 : 4;
+    for (int t = 2 * rank + tid / BN; t < nt; t += U * step) {
+      float v[U] = {}, u[U] = {};
+      for (int r = 0; r < split; r += 4) {
+        float pv[4][U], pu[4][U];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (r + q >= split) break;
+          const uint32_t p = mapa_shared(p0, (uint32_t)(r + q));
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int ti = min(t + i * step, nt - 1);
+            pv[q][i] = ld_cluster_f32(p + (uint32_t)ti * BN * 4);
+            if (GATED) pu[q][i] = ld_cluster_f32(p + m3 + (uint32_t)ti * BN * 4);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (r + q >= split) break;
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            v[i] += pv[q][i];
+            if (GATED) u[i] += pu[q][i];
+          }
+        }
       }
       if (!in) continue;
-      const int64_t m = t0 + t;
-      v += b;
-      if (P.pre) from_f32(static_cast<T *>(P.pre)[m * P.N + n], v);
-      with_act(P.act, [&](auto A) { v = act_fwd<true, decltype(A)::value>(v); });
-      if (GATED) {
-        u += b3;
-        if (P.pre3) from_f32(static_cast<T *>(P.pre3)[m * P.N + n], u);
-        v *= u;
-      } else if (P.residual) {
-        v += to_f32(static_cast<const T *>(P.residual)[m * P.ld_r + n]);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (t + i * step >= nt) break;
+        const int64_t m = t0 + t + i * step;
+        float y = v[i] + b;
+        if (P.pre) from_f32(static_cast<T *>(P.pre)[m * P.N + n], y);
+        with_act(P.act, [&](auto A) { y = act_fwd<true, decltype(A)::value>(y); });
+        if (GATED) {
+          const float w = u[i] + b3;
+          if (P.pre3) from_f32(static_cast<T *>(P.pre3)[m * P.N + n], w);
+          y *= w;
+        } else if (P.residual) {
+          y += to_f32(static_cast<const T *>(P.residual)[m * P.ld_r + n]);
+        }
+        from_f32(static_cast<T *>(P.out)[m * P.ld_o + n], y);
       }
-      from_f32(static_cast<T *>(P.out)[m * P.ld_o + n], v);
     }
   }
   cluster_sync_all();              // no CTA leaves while another may read its partial tile
@@ -248,9 +275,12 @@ cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, s
 
 }  // namespace
 
+#ifndef DF_MAX_M
+#define DF_MAX_M 128
+#endif
 // Tokens up to which this kernel takes a forward product
 bool dense_few_ok(const DenseGemm &g) {
-  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.M <= 128 && dense_tc_ok(g);
+  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.M <= DF_MAX_M && dense_tc_ok(g);
 }
 
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {
@@ -259,9 +289,10 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   FewParams P{};
   P.tt = (int)std::min<int64_t>(128, (g.M + 15) / 16 * 16);
   const size_t stage = (size_t)nw * kWBytes + (size_t)P.tt * BK * 2;
-  // two CTAs an SM where that leaves each at least three stages
+  // two CTAs an SM, at least two stages each: with 80 KB and more in flight a
+  // CTA the stream needs no deeper ring
   const size_t half = 108 * 1024;
-  const bool two = 3 * stage <= half;
+  const bool two = 2 * stage <= half && (size_t)nw * P.tt * BN * 4 <= half;
   P.stages = (int)std::min<size_t>(kMaxStages, (two ? half : kMaxSmem - 1024) / stage);
   P.KB = (int)((g.K + BK - 1) / BK);
   const int64_t tiles = (g.N + BN - 1) / BN, ttiles = (g.M + P.tt - 1) / P.tt;
