@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -121,8 +122,9 @@ def lib() -> ctypes.CDLL:
             "moe_gated_ffn": [ctypes.POINTER(MoeGatedFfnConfig)] + [vp] * 12 + [sz, vp],
             "moe_gated_ffn_backward": [ctypes.POINTER(MoeGatedFfnConfig)] + [vp] * 15 + [sz, vp],
             "moe_query_clip_size": [ctypes.c_int32, ctypes.POINTER(sz)],
-            "moe_grad_norm": [ctypes.POINTER(MoeGrad), ctypes.c_int32, vp, vp, sz, vp],
-            "moe_clip_grads": [ctypes.POINTER(MoeGrad), ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp],
+            # (the list as its bytes)
+            "moe_grad_norm": [ctypes.c_char_p, ctypes.c_int32, vp, vp, sz, vp],
+            "moe_clip_grads": [ctypes.c_char_p, ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -592,31 +594,55 @@ def _moe_dtype(dtype: torch.dtype) -> int:
 def _on_device(t: torch.Tensor) -> None:
     if not t.is_cuda:
         raise ValueError("libmoe takes CUDA tensors only (no CPU path)")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"tensor on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
 
 
-def _rows(t: torch.Tensor | None, rows: int, width: int, ld: int, dtype: int):
-    """Device pointer of a [rows, width] tensor whose rows are `ld` elements
-    apart (0: packed) and contiguous within themselves."""
-    if t is None:
-        return None
-    _on_device(t)
-    if _DTYPES.get(t.dtype) != dtype:
-        raise ValueError(f"{t.dtype} tensor, but the configuration's dtype is another")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
-        raise ValueError(f"expected [{rows}, {width}], got {list(t.shape)}")
-    if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or width)):
-        raise ValueError(f"strides {t.stride()}, but the configuration's rows are {ld or width} apart")
-    return t.data_ptr()
+class _Args:
+    """Checks of one call's tensors against the call's dtype and device.  The
+    calls below launch work of a few microseconds, so a tensor that is as
+    expected passes on four comparisons; what is wrong is found out after."""
 
+    __slots__ = ("dev", "dtype")
 
-def _vec(t: torch.Tensor | None, n: int, dtype: int):
-    """Device pointer of a contiguous vector of n elements."""
-    if t is None:
-        return None
-    return _rows(t.view(1, -1) if t.dim() == 1 else t, 1, n, 0, dtype)
+    def __init__(self, dtype: int):
+        self.dev = torch.cuda.current_device()
+        self.dtype = torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+
+    def rows(self, t: torch.Tensor | None, rows: int, width: int, ld: int):
+        """Device pointer of a [rows, width] tensor whose rows are `ld` elements
+        apart (0: packed) and contiguous within themselves."""
+        if t is None:
+            return None
+        if (t.get_device() == self.dev and t.dtype is self.dtype and t.shape == (rows, width)
+                and t.stride() == (ld or width, 1)):
+            return t.data_ptr()
+        _on_device(t)
+        if t.dtype != self.dtype:
+            raise ValueError(f"{t.dtype} tensor, but the configuration's dtype is {self.dtype}")
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+            raise ValueError(f"expected [{rows}, {width}], got {list(t.shape)}")
+        if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or width)):
+            raise ValueError(f"strides {t.stride()}, but the configuration's rows are {ld or width} apart")
+        return t.data_ptr()
+
+    def vec(self, t: torch.Tensor | None, n: int):
+        """Device pointer of a contiguous vector of n elements."""
+        if t is None:
+            return None
+        return self.rows(t.view(1, -1) if t.dim() == 1 else t, 1, n, 0)
+
+    def stream(self, stream: torch.cuda.Stream | None) -> int:
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.dev)
+
+    def workspace(self, ws: torch.Tensor):
+        if ws.get_device() != self.dev or not ws.is_contiguous():
+            _on_device(ws)
+            raise ValueError("libmoe takes contiguous tensors")
+        return ws.data_ptr(), ws.nbytes
 
 
 def linear_config(M: int, K: int, N: int, act: str = "identity", dtype: torch.dtype = torch.bfloat16,
@@ -660,61 +686,72 @@ def new_gated_ffn_workspace(cfg: MoeGatedFfnConfig, backward: bool = False, devi
 
 def moe_linear(cfg, x, w, bias, residual, y, z, ws, stream=None):
     """y = act(x w^T + bias) + residual; z (or None) receives x w^T + bias."""
-    wp, wn = _ws(ws)
-    c, dt = cfg, cfg.dtype
+    M, K, N, q = cfg.M, cfg.K, cfg.N, _Args(cfg.dtype)
+    wp, wn = q.workspace(ws)
     _check("moe_linear", lib().moe_linear(
-        ctypes.byref(c), _rows(x, c.M, c.K, c.ld_x, dt), _rows(w, c.N, c.K, c.ld_w, dt), _vec(bias, c.N, dt),
-        _rows(residual, c.M, c.N, c.ld_r, dt), _rows(y, c.M, c.N, c.ld_y, dt), _rows(z, c.M, c.N, 0, dt),
-        wp, wn, _stream(stream)))
+        ctypes.byref(cfg), q.rows(x, M, K, cfg.ld_x), q.rows(w, N, K, cfg.ld_w), q.vec(bias, N),
+        q.rows(residual, M, N, cfg.ld_r), q.rows(y, M, N, cfg.ld_y), q.rows(z, M, N, 0), wp, wn,
+        q.stream(stream)))
 
 
 def moe_linear_backward(cfg, x, w, z, dy, dx, dw, dbias, ws, stream=None):
     """Gradients of sum(dy * y): dx, dw, dbias (each may be None)."""
-    wp, wn = _ws(ws)
-    c, dt = cfg, cfg.dtype
+    M, K, N, q = cfg.M, cfg.K, cfg.N, _Args(cfg.dtype)
+    wp, wn = q.workspace(ws)
     _check("moe_linear_backward", lib().moe_linear_backward(
-        ctypes.byref(c), _rows(x, c.M, c.K, c.ld_x, dt), _rows(w, c.N, c.K, c.ld_w, dt),
-        _rows(z, c.M, c.N, 0, dt), _rows(dy, c.M, c.N, c.ld_y, dt), _rows(dx, c.M, c.K, c.ld_x, dt),
-        _rows(dw, c.N, c.K, 0, dt), _vec(dbias, c.N, dt), wp, wn, _stream(stream)))
+        ctypes.byref(cfg), q.rows(x, M, K, cfg.ld_x), q.rows(w, N, K, cfg.ld_w), q.rows(z, M, N, 0),
+        q.rows(dy, M, N, cfg.ld_y), q.rows(dx, M, K, cfg.ld_x), q.rows(dw, N, K, 0), q.vec(dbias, N), wp, wn,
+        q.stream(stream)))
 
 
 def moe_gated_ffn(cfg, x, w1, b1, w3, b3, w2, b2, residual, y, a, u, ws, stream=None):
     """y = (act(x w1^T + b1) * (x w3^T + b3)) w2^T + b2 + residual; a, u (or
     None) receive the two pre-activations for the backward pass."""
-    wp, wn = _ws(ws)
-    T, d, f, dt = cfg.T, cfg.d_model, cfg.d_ff, cfg.dtype
+    T, d, f, q = cfg.T, cfg.d_model, cfg.d_ff, _Args(cfg.dtype)
+    wp, wn = q.workspace(ws)
     _check("moe_gated_ffn", lib().moe_gated_ffn(
-        ctypes.byref(cfg), _rows(x, T, d, cfg.ld_x, dt), _rows(w1, f, d, 0, dt), _vec(b1, f, dt),
-        _rows(w3, f, d, 0, dt), _vec(b3, f, dt), _rows(w2, d, f, 0, dt), _vec(b2, d, dt),
-        _rows(residual, T, d, cfg.ld_r, dt), _rows(y, T, d, cfg.ld_y, dt), _rows(a, T, f, 0, dt),
-        _rows(u, T, f, 0, dt), wp, wn, _stream(stream)))
+        ctypes.byref(cfg), q.rows(x, T, d, cfg.ld_x), q.rows(w1, f, d, 0), q.vec(b1, f), q.rows(w3, f, d, 0),
+        q.vec(b3, f), q.rows(w2, d, f, 0), q.vec(b2, d), q.rows(residual, T, d, cfg.ld_r),
+        q.rows(y, T, d, cfg.ld_y), q.rows(a, T, f, 0), q.rows(u, T, f, 0), wp, wn, q.stream(stream)))
 
 
 def moe_gated_ffn_backward(cfg, x, w1, w3, w2, a, u, dy, dx, dw1, db1, dw3, db3, dw2, db2, ws, stream=None):
     """Gradients of sum(dy * y) from the forward's a and u (outputs may be None)."""
-    wp, wn = _ws(ws)
-    T, d, f, dt = cfg.T, cfg.d_model, cfg.d_ff, cfg.dtype
+    T, d, f, q = cfg.T, cfg.d_model, cfg.d_ff, _Args(cfg.dtype)
+    wp, wn = q.workspace(ws)
     _check("moe_gated_ffn_backward", lib().moe_gated_ffn_backward(
-        ctypes.byref(cfg), _rows(x, T, d, cfg.ld_x, dt), _rows(w1, f, d, 0, dt), _rows(w3, f, d, 0, dt),
-        _rows(w2, d, f, 0, dt), _rows(a, T, f, 0, dt), _rows(u, T, f, 0, dt), _rows(dy, T, d, cfg.ld_y, dt),
-        _rows(dx, T, d, cfg.ld_x, dt), _rows(dw1, f, d, 0, dt), _vec(db1, f, dt), _rows(dw3, f, d, 0, dt),
-        _vec(db3, f, dt), _rows(dw2, d, f, 0, dt), _vec(db2, d, dt), wp, wn, _stream(stream)))
+        ctypes.byref(cfg), q.rows(x, T, d, cfg.ld_x), q.rows(w1, f, d, 0), q.rows(w3, f, d, 0),
+        q.rows(w2, d, f, 0), q.rows(a, T, f, 0), q.rows(u, T, f, 0), q.rows(dy, T, d, cfg.ld_y),
+        q.rows(dx, T, d, cfg.ld_x), q.rows(dw1, f, d, 0), q.vec(db1, f), q.rows(dw3, f, d, 0), q.vec(db3, f),
+        q.rows(dw2, d, f, 0), q.vec(db2, d), wp, wn, q.stream(stream)))
 
 
 def _grad_list(grads, out=None):
-    """The C list of a sequence of contiguous CUDA tensors (None entries are skipped)."""
-    pairs = [(g, o) for g, o in zip(grads, out if out is not None else grads, strict=True) if g is not None]
-    arr = (MoeGrad * max(1, len(pairs)))()
-    for e, (g, o) in zip(arr, pairs):
-        _on_device(g)
-        if not g.is_contiguous():
+    """The C list of a sequence of contiguous CUDA tensors (None entries are
+    skipped): the bytes of moe_grad entries, and their number."""
+    dev, vals, n = None, [], 0
+    for g, o in zip(grads, out if out is not None else grads, strict=True):
+        if g is None:
+            continue
+        dt = _DTYPES.get(g.dtype)
+        if dev is None:
+            _on_device(g)
+            dev = g.get_device()
+        if g.get_device() != dev or dt is None or not g.is_contiguous():
+            _on_device(g)
+            _moe_dtype(g.dtype)
             raise ValueError("libmoe takes contiguous gradients")
+        src, size = g.data_ptr(), g.numel()
+        dst = src
         if o is not g:
-            _on_device(o)
-            if not o.is_contiguous() or o.dtype != g.dtype or o.numel() != g.numel():
+            if o.get_device() != dev:
+                _on_device(o)
+            if not o.is_contiguous() or o.dtype != g.dtype or o.numel() != size:
                 raise ValueError("each output is a contiguous tensor of its gradient's size and dtype")
-        e.src, e.dst, e.n, e.dtype = g.data_ptr(), o.data_ptr(), g.numel(), _moe_dtype(g.dtype)
-    return arr, len(pairs)
+            dst = o.data_ptr()
+        vals += (src, dst, size, dt, 0)
+        n += 1
+    return struct.pack("=" + "QQqii" * n, *vals), n
 
 
 def new_clip_workspace(grads, device="cuda") -> torch.Tensor:
@@ -725,9 +762,9 @@ def new_clip_workspace(grads, device="cuda") -> torch.Tensor:
 def moe_grad_norm(grads, norm, ws, stream=None):
     """norm (one fp32 element) = sqrt of the sum of squares over all tensors of the list."""
     arr, n = _grad_list(grads)
-    wp, wn = _ws(ws)
-    _check("moe_grad_norm", lib().moe_grad_norm(arr, n, _ptr(norm, 1, torch.float32), wp, wn,
-                                                _stream(stream)))
+    q = _Args(MOE_F32)
+    wp, wn = q.workspace(ws)
+    _check("moe_grad_norm", lib().moe_grad_norm(arr, n, _ptr(norm, 1, torch.float32), wp, wn, q.stream(stream)))
 
 
 def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
@@ -735,9 +772,10 @@ def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
     place or into the tensors of `out`; norm (or None) receives the norm
     before clipping."""
     arr, n = _grad_list(grads, out)
-    wp, wn = _ws(ws)
-    _check("moe_clip_grads", lib().moe_clip_grads(arr, n, float(max_norm), _ptr(norm, 1, torch.float32), wp, wn,
-                                                  _stream(stream)))
+    q = _Args(MOE_F32)
+    wp, wn = q.workspace(ws)
+    _check("moe_clip_grads", lib().moe_clip_grads(arr, n, max_norm, _ptr(norm, 1, torch.float32), wp, wn,
+                                                  q.stream(stream)))
 
 
 class GatedFFN:

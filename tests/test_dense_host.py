@@ -135,7 +135,7 @@ def grads(*entries):
     arr = (api.MoeGrad * max(1, len(entries)))()
     for e, (src, dst, n, dt) in zip(arr, entries):
         e.src, e.dst, e.n, e.dtype = src, dst, n, dt
-    return arr, len(entries)
+    return bytes(arr), len(entries)
 
 
 def test_clip_refusals(L):
@@ -206,7 +206,5 @@ def test_binding_refuses_cpu_tensors_and_unknown_options(L):
     with pytest.raises(ValueError):
         api.gated_ffn_config(1, 2, 3, dtype=torch.float16)
     t = torch.zeros(4, 4)
-    with pytest.raises(ValueError):
-        api._rows(t, 4, 4, 0, api.MOE_F32)
     with pytest.raises(ValueError):
         api._grad_list([t])
