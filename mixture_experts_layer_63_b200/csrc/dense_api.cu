@@ -101,31 +101,110 @@ moe_status validate_linear(const moe_linear_config *in, moe_linear_config *c) {
   return MOE_OK;
 }
 
+// Room for the tensor cores' copy of a [lines, inner] matrix whose lines are
+// ld elements apart: fp32 matrices (their planes) and bf16 ones with lines
+// that are not 16-byte aligned.
+size_t pack_room(int dtype, int64_t lines, int64_t inner, int64_t ld) {
+  if (dtype == MOE_BF16 && (lines <= 1 || ld % 8 == 0)) return 0;
+  return align256(pack_bytes(dtype, lines, inner));
+}
+
 struct LinearLayout {
-  size_t dz, part, total;
+  size_t dz, part, pack, total;
 };
 
 LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
   LinearLayout L{};
   Taker t;
+  size_t room = pack_room(c.dtype, c.M, c.K, c.ld_x) + pack_room(c.dtype, c.N, c.K, c.ld_w);
   if (backward) {
-    L.dz = t.take(c.act != MOE_DENSE_IDENTITY ? (size_t)c.M * c.N * dense_elem(c.dtype) : 0);
+    const bool act = c.act != MOE_DENSE_IDENTITY;
+    L.dz = t.take(act ? (size_t)c.M * pack_ld(c.N) * dense_elem(c.dtype) : 0);
     L.part = t.take(colsum_scratch(c.M, c.N, 1));
+    room += pack_room(c.dtype, c.M, c.N, act ? pack_ld(c.N) : c.ld_y);
   }
+  L.pack = t.take(room);
   L.total = t.o;
   return L;
 }
 
-// n products of one kind: on the tensor cores where all of them fit there
-cudaError_t run_products(const DenseGemm *g, int n, char *ws, cudaStream_t s) {
-  if (n == 1 && dense_few_ok(g[0])) return launch_dense_few(g[0], reinterpret_cast<uint32_t *>(ws), s);
-  bool tc = true;
-  for (int i = 0; i < n; ++i) tc = tc && dense_tc_ok(g[i]);
-  if (tc) return launch_dense_tc(g, n, reinterpret_cast<uint32_t *>(ws), s);
-  cudaError_t e = cudaSuccess;
-  for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_dense_simt(g[i], s);
-  return e;
-}
+// The products of one call: each group of up to four with one epilogue runs
+// on the kernel that suits it.  Copies made for the tensor cores stay for the
+// later groups of the call.
+class Products {
+ public:
+  Products(int dtype, void *ws, size_t pack, size_t end, cudaStream_t s)
+      : dtype_(dtype), base_(static_cast<char *>(ws)), at_(pack), end_(end), s_(s) {}
+
+  cudaError_t run(DenseGemm *g, int n) {
+    uint32_t *err = reinterpret_cast<uint32_t *>(base_);
+    if (n == 1 && dense_few_ok(g[0])) return launch_dense_few(g[0], err, s_);
+    double macs = 0;
+    for (int i = 0; i < n; ++i) macs += (double)g[i].M * g[i].N * g[i].K * (g[i].a2.p || g[i].b3.p ? 2 : 1);
+    if (macs >= kTcMacs || dtype_ == MOE_BF16) {
+      DenseGemm q[4];
+      bool ok = true;
+      for (int i = 0; i < n && ok; ++i) {
+        q[i] = g[i];
+        ok = prepare(&q[i].a, g[i].M, g[i].K) && prepare(&q[i].b, g[i].N, g[i].K) &&
+             prepare(&q[i].b3, g[i].N, g[i].K) && prepare(&q[i].a2, g[i].M, g[i].K) &&
+             prepare(&q[i].b2, g[i].N, g[i].K) && dense_tc_ok(q[i]);
+      }
+      if (ok) {
+        cudaError_t e = cudaSuccess;
+        if (launched_ < jobs_) e = launch_pack(dtype_, job_ + launched_, jobs_ - launched_, s_);
+        launched_ = jobs_;
+        if (e != cudaSuccess) return e;
+        if (n == 1 && dense_few_ok(q[0])) return launch_dense_few(q[0], err, s_);
+        return launch_dense_tc(q, n, err, s_);
+      }
+      jobs_ = launched_;
+    }
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_dense_simt(g[i], s_);
+    return e;
+  }
+  cudaError_t run(DenseGemm &g) { return run(&g, 1); }
+
+ private:
+  // fewer multiply-adds than this stay on the CUDA cores in fp32: the splits
+  // and the tensor-core launch cost more than they save
+  static constexpr double kTcMacs = 1 << 22;
+  static constexpr int kMaxJobs = 8;
+
+  // `o`, rows x K, replaced by its copy where the tensor cores need one
+  bool prepare(Operand *o, int64_t rows, int64_t K) {
+    if (!o->p || rows == 0 || K == 0) return true;
+    const bool km = o->ks == 1;
+    const int64_t lines = km ? rows : K, inner = km ? K : rows, ld = km ? o->rs : o->ks;
+    if (pack_room(dtype_, lines, inner, ld) == 0) return true;
+    int j = 0;
+    while (j < jobs_ && !(job_[j].src == o->p && job_[j].lines == lines && job_[j].inner == inner &&
+                          job_[j].ld == ld))
+      ++j;
+    if (j == jobs_) {
+      const size_t need = align256(pack_bytes(dtype_, lines, inner));
+      if (jobs_ == kMaxJobs || jobs_ - launched_ == kMaxPack || at_ + need > end_) return false;
+      job_[jobs_++] = {o->p, lines, inner, ld, base_ + at_};
+      at_ += need;
+    }
+    o->p = job_[j].dst;
+    (km ? o->rs : o->ks) = pack_ld(inner);
+    if (dtype_ == MOE_F32) {
+      o->planes = 3;
+      o->plane_stride = lines * pack_ld(inner);
+    }
+    return true;
+  }
+
+  int dtype_;
+  char *base_;
+  size_t at_, end_;
+  cudaStream_t s_;
+  PackJob job_[kMaxJobs];
+  int jobs_ = 0, launched_ = 0;
+};
+
 // out [M, N] = sum over k < K of a(m, k) b(n, k)
 DenseGemm product(int dtype, int64_t M, int64_t K, int32_t N, const Operand &a, const Operand &b, void *out,
                   int64_t ld_o) {
@@ -141,7 +220,6 @@ DenseGemm product(int dtype, int64_t M, int64_t K, int32_t N, const Operand &a, 
   g.ld_o = ld_o;
   return g;
 }
-cudaError_t run_product(const DenseGemm &g, char *ws, cudaStream_t s) { return run_products(&g, 1, ws, s); }
 
 // ---- gated block ------------------------------------------------------------------
 moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *c) {
@@ -160,19 +238,25 @@ moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *
 }
 
 struct GatedLayout {
-  size_t h, da, du, part, total;
+  size_t h, da, du, part, pack, total;
 };
 
 GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
   GatedLayout L{};
   Taker t;
-  const size_t tf = (size_t)c.T * c.d_ff * dense_elem(c.dtype);
+  // h, dA and dU have aligned lines of their own
+  const int64_t T = c.T, d = c.d_model, f = c.d_ff, ldh = pack_ld(f);
+  const size_t tf = (size_t)T * ldh * dense_elem(c.dtype);
+  auto room = [&](int64_t lines, int64_t inner, int64_t ld) { return pack_room(c.dtype, lines, inner, ld); };
+  size_t pack = room(T, d, c.ld_x) + 2 * room(f, d, d) + room(d, f, f) + room(T, f, ldh);
   L.h = t.take(tf);
   if (backward) {
     L.da = t.take(tf);
     L.du = t.take(tf);
-    L.part = t.take(colsum_scratch(c.T, std::max(c.d_ff, c.d_model), 3));
+    L.part = t.take(colsum_scratch(T, std::max(c.d_ff, c.d_model), 3));
+    pack += 2 * room(T, f, ldh) + room(T, d, c.ld_y);
   }
+  L.pack = t.take(pack);
   L.total = t.o;
   return L;
 }
@@ -223,7 +307,8 @@ moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *w
   g.out = y;
   g.ld_o = c.ld_y;
   g.pre = z;
-  return dense_status(run_product(g, static_cast<char *>(ws), reinterpret_cast<cudaStream_t>(stream)));
+  Products run(c.dtype, ws, L.pack, L.total, reinterpret_cast<cudaStream_t>(stream));
+  return dense_status(run.run(g));
 }
 
 moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, const void *w, const void *z,
@@ -250,15 +335,16 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
   Operand dz{dy, c.ld_y, 1};
   if (act || dbias) {
     // dz and its column sums in one pass over dy and z
-    const ColSum q{dy, c.ld_y, c.N, act ? z : nullptr, act ? base + L.dz : nullptr, dbias};
+    const ColSum q{dy, c.ld_y, c.N, act ? z : nullptr, act ? base + L.dz : nullptr, pack_ld(c.N), dbias};
     e = launch_colsums(c.act, c.dtype, c.M, &q, 1, reinterpret_cast<float *>(base + L.part), s);
-    if (act) dz = {base + L.dz, c.N, 1};
+    if (act) dz = {base + L.dz, pack_ld(c.N), 1};
   }
   DenseGemm g[2] = {};
   int n = 0;
   if (dx && c.M > 0) g[n++] = product(c.dtype, c.M, c.N, c.K, dz, {w, 1, c.ld_w}, dx, c.ld_x);
   if (dw) g[n++] = product(c.dtype, c.N, c.M, c.K, {dz.p, 1, dz.rs}, {x, 1, c.ld_x}, dw, c.K);
-  if (e == cudaSuccess && n > 0) e = run_products(g, n, base, s);
+  Products run(c.dtype, ws, L.pack, L.total, s);
+  if (e == cudaSuccess && n > 0) e = run.run(g, n);
   return dense_status(e);
 }
 
@@ -283,7 +369,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   if (c.T == 0) return MOE_OK;
   if (!x || !w1 || !w3 || !w2 || !y || !b1 != !b3 || !a != !u) return MOE_ERR_INVALID_ARG;
   const int es = (int)dense_elem(c.dtype);
-  const int64_t T = c.T, d = c.d_model, f = c.d_ff;
+  const int64_t T = c.T, d = c.d_model, f = c.d_ff, ldh = pack_ld(f);
   const bool in_place = residual == y && c.ld_r == c.ld_y;
   const Span sr{residual, T, d, c.ld_r, es};
   if ((st = check_spans({Span{x, T, d, c.ld_x, es}, Span{w1, f, d, d, es}, Span{w3, f, d, d, es},
@@ -306,10 +392,11 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   g.bias = b1;
   g.bias3 = b3;
   g.out = base + L.h;
-  g.ld_o = f;
+  g.ld_o = ldh;
   g.pre = a;
   g.pre3 = u;
-  cudaError_t e = run_product(g, base, s);
+  Products run(c.dtype, ws, L.pack, L.total, s);
+  cudaError_t e = run.run(g);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm q{};
   q.epi = kDenseLinear;
@@ -318,14 +405,14 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   q.M = T;
   q.N = c.d_model;
   q.K = f;
-  q.a = {base + L.h, f, 1};
+  q.a = {base + L.h, ldh, 1};
   q.b = {w2, f, 1};
   q.bias = b2;
   q.residual = residual;
   q.ld_r = c.ld_r;
   q.out = y;
   q.ld_o = c.ld_y;
-  return dense_status(run_product(q, base, s));
+  return dense_status(run.run(q));
 }
 
 moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x, const void *w1,
@@ -343,7 +430,7 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   if (c.T > 0 && (!dy || (hidden && (!w2 || !a || !u)) || (dw1 && !x) || (dx && (!w1 || !w3))))
     return MOE_ERR_INVALID_ARG;
   const int es = (int)dense_elem(c.dtype);
-  const int64_t T = c.T, d = c.d_model, f = c.d_ff;
+  const int64_t T = c.T, d = c.d_model, f = c.d_ff, ldh = pack_ld(f);
   if ((st = check_spans({Span{x, T, d, c.ld_x, es}, Span{w1, f, d, d, es}, Span{w3, f, d, d, es},
                          Span{w2, d, f, f, es}, Span{a, T, f, f, es}, Span{u, T, f, f, es},
                          Span{dy, T, d, c.ld_y, es}},
@@ -356,6 +443,7 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   char *h = base + L.h, *da = base + L.da, *du = base + L.du;
   float *part = reinterpret_cast<float *>(base + L.part);
   cudaError_t e = cudaSuccess;
+  Products run(c.dtype, ws, L.pack, L.total, s);
   if (hidden && T > 0) {
     DenseGemm g{};
     g.epi = kDenseGatedGrad;
@@ -369,30 +457,30 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
     g.pre_in = a;
     g.pre3_in = u;
     g.out = da;
-    g.ld_o = f;
+    g.ld_o = ldh;
     g.out2 = du;
     g.out3 = h;
-    e = run_product(g, base, s);
+    e = run.run(g);
   }
   // dx and the weight gradients (each contracts two matrices over the rows) in one launch
   DenseGemm g[4] = {};
   int n = 0;
   if (dx && T > 0) {
-    g[n] = product(c.dtype, T, f, c.d_model, {da, f, 1}, {w1, 1, d}, dx, c.ld_x);
-    g[n].a2 = {du, f, 1};
+    g[n] = product(c.dtype, T, f, c.d_model, {da, ldh, 1}, {w1, 1, d}, dx, c.ld_x);
+    g[n].a2 = {du, ldh, 1};
     g[n++].b2 = {w3, 1, d};
   }
   if (dw1) {
-    g[n++] = product(c.dtype, f, T, c.d_model, {da, 1, f}, {x, 1, c.ld_x}, dw1, d);
-    g[n++] = product(c.dtype, f, T, c.d_model, {du, 1, f}, {x, 1, c.ld_x}, dw3, d);
+    g[n++] = product(c.dtype, f, T, c.d_model, {da, 1, ldh}, {x, 1, c.ld_x}, dw1, d);
+    g[n++] = product(c.dtype, f, T, c.d_model, {du, 1, ldh}, {x, 1, c.ld_x}, dw3, d);
   }
-  if (dw2) g[n++] = product(c.dtype, d, T, c.d_ff, {dy, 1, c.ld_y}, {h, 1, f}, dw2, f);
-  if (e == cudaSuccess && n > 0) e = run_products(g, n, base, s);
+  if (dw2) g[n++] = product(c.dtype, d, T, c.d_ff, {dy, 1, c.ld_y}, {h, 1, ldh}, dw2, f);
+  if (e == cudaSuccess && n > 0) e = run.run(g, n);
   ColSum bq[3];
   int nb = 0;
-  if (db1) bq[nb++] = {da, f, c.d_ff, nullptr, nullptr, db1};
-  if (db3) bq[nb++] = {du, f, c.d_ff, nullptr, nullptr, db3};
-  if (db2) bq[nb++] = {dy, c.ld_y, c.d_model, nullptr, nullptr, db2};
+  if (db1) bq[nb++] = {da, ldh, c.d_ff, nullptr, nullptr, 0, db1};
+  if (db3) bq[nb++] = {du, ldh, c.d_ff, nullptr, nullptr, 0, db3};
+  if (db2) bq[nb++] = {dy, c.ld_y, c.d_model, nullptr, nullptr, 0, db2};
   if (e == cudaSuccess && nb > 0) e = launch_colsums(0, c.dtype, T, bq, nb, part, s);
   return dense_status(e);
 }

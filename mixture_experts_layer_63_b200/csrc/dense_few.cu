@@ -280,7 +280,7 @@ cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, s
 #endif
 // Tokens up to which this kernel takes a forward product
 bool dense_few_ok(const DenseGemm &g) {
-  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.M <= DF_MAX_M && dense_tc_ok(g);
+  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.dtype == MOE_BF16 && g.M <= DF_MAX_M && dense_tc_ok(g);
 }
 
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {

@@ -10,9 +10,13 @@ namespace moe {
 // A matrix operand of a product: element (row, k) at p + row * rs + k * ks
 // (strides in elements).  ks == 1: the contraction index is contiguous
 // (K-major); rs == 1: the rows are (MN-major).
+// planes: bf16 matrices plane_stride elements apart whose sum is the operand
+// (0: p has the product's own dtype)
 struct Operand {
   const void *p;
   int64_t rs, ks;
+  int planes;
+  int64_t plane_stride;
 };
 
 enum DenseEpilogue : int {
@@ -39,7 +43,7 @@ struct DenseGemm {
   int64_t ld_o;
   void *pre, *pre3;              // [M, N] packed, or null
   const void *pre_in, *pre3_in;  // [M, N] packed
-  void *out2, *out3;             // [M, N] packed
+  void *out2, *out3;             // rows ld_o apart
 };
 
 inline size_t dense_elem(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
@@ -47,19 +51,36 @@ inline size_t dense_elem(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 // CUDA-core product (dense_simt.cu): any strides, any sizes
 cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 
-// Tensor-core products (dense_tc.cu).  dense_tc_ok: bf16 operands whose base
-// and lines are 16-byte aligned.  launch_dense_tc runs up to four products with
-// one epilogue in one launch.
+// Tensor-core products (dense_tc.cu).  dense_tc_ok: every operand is bf16 (or
+// bf16 planes) with base and lines 16-byte aligned.  launch_dense_tc runs up
+// to four products with one epilogue in one launch.
 bool dense_tc_ok(const DenseGemm &g);
 cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
+
+// Copies of matrices for the tensor cores (dense_pack.cu): `lines` lines of
+// `inner` elements, ld apart, into bf16 planes of round_up(inner, 8) elements a
+// line: one plane (bf16, to align the lines) or the three planes of an fp32
+// matrix.  Up to kMaxPack matrices in one launch.
+constexpr int kMaxPack = 6;
+struct PackJob {
+  const void *src;
+  int64_t lines, inner, ld;
+  void *dst;
+};
+__host__ __device__ inline int64_t pack_ld(int64_t inner) { return (inner + 7) / 8 * 8; }
+inline size_t pack_bytes(int dtype, int64_t lines, int64_t inner) {
+  return (size_t)(lines * pack_ld(inner)) * 2 * (dtype == MOE_F32 ? 3 : 1);
+}
+cudaError_t launch_pack(int dtype, const PackJob *jobs, int n, cudaStream_t s);
 
 // Forward products of few rows (dense_few.cu)
 bool dense_few_ok(const DenseGemm &g);
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s);
 
 // Column sums out[n] = sum_m src[m, n] (fp32, in a fixed order), up to three
-// matrices of M rows in one launch.  With z and dz (packed [M, N]):
-// dz = src * act'(z) first, and the sums are dz's; out may then be null.
+// matrices of M rows in one launch.  With z (packed [M, N])
+// and dz (lines ld_dz apart): dz = src * act'(z) first, and the sums are dz's;
+// out may then be null.
 // part: scratch of colsum_scratch(M, widest N, count) bytes.
 constexpr int kMaxColSums = 3;
 struct ColSum {
@@ -67,7 +88,9 @@ struct ColSum {
   int64_t ld;
   int N;
   const void *z;
-  void *dz, *out;
+  void *dz;
+  int64_t ld_dz;
+  void *out;
 };
 size_t colsum_scratch(int64_t M, int N, int count);
 cudaError_t launch_colsums(int act, int dtype, int64_t M, const ColSum *q, int count, float *part,

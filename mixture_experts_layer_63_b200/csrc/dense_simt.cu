@@ -68,8 +68,8 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
       float f = 0.0f, d = 0.0f;
       with_act(P.act, [&](auto A) { act_both<FAST, decltype(A)::value>(a, f, d); });
       from_f32(*out, acc * u * d);
-      from_f32(static_cast<T *>(P.out2)[at], acc * f);
-      from_f32(static_cast<T *>(P.out3)[at], f * u);
+      from_f32(static_cast<T *>(P.out2)[m * P.ld_o + n], acc * f);
+      from_f32(static_cast<T *>(P.out3)[m * P.ld_o + n], f * u);
       break;
     }
     default: from_f32(*out, acc);
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
             act_both<sizeof(T) == 2, ACT>(zz[j], f, d);
             v[j] *= d;
           }
-          *reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.N + n) = pack16<T>(v);
+          *reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.ld_dz + n) = pack16<T>(v);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += v[j];
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256) colsum_part_kernel(const ColSums P) {
           float f, d;
           act_both<sizeof(T) == 2, ACT>(to_f32(z[r * Q.N + c]), f, d);
           v *= d;
-          from_f32(dz[r * Q.N + c], v);
+          from_f32(dz[r * Q.ld_dz + c], v);
         }
         sum[j] += v;
       }

@@ -357,8 +357,8 @@ struct Epilogue {
         });
         __syncwarp();
         store_chunk(out, row0, col, da, stg, lane);
-        store_chunk(packed(Q.out2), row0, col, du, stg_u, lane);
-        store_chunk(packed(Q.out3), row0, col, hh, stg, lane);
+        store_chunk(Rows<T>(Q.out2, Q.ld_o, Q.M, Q.N), row0, col, du, stg_u, lane);
+        store_chunk(Rows<T>(Q.out3, Q.ld_o, Q.M, Q.N), row0, col, hh, stg, lane);
       }
     }
   }
@@ -628,6 +628,16 @@ cudaError_t launch_pair_as(const TcParams &P, cudaStream_t s) {
   return launch_kernel(kern, 2 * (unsigned)std::min<int>(pairs, P.pr[P.nprob - 1].tile_end), kThreads, smem, s, P);
 }
 
+template <typename T>
+cudaError_t launch_as(int epi, const TcParams &P, cudaStream_t s) {
+  switch (epi) {
+    case kDenseLinear: return launch_pair_as<kDenseLinear, T>(P, s);
+    case kDenseGated: return launch_pair_as<kDenseGated, T>(P, s);
+    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, T>(P, s);
+    default: return launch_pair_as<kDenseStore, T>(P, s);
+  }
+}
+
 bool kmajor(const Operand &o) { return o.ks == 1; }
 
 // `rows` x K bf16 operand for TMA: 16-byte aligned base and lines
@@ -639,23 +649,26 @@ bool tma_ok(const Operand &o, int64_t rows, int64_t K) {
 
 // Map {inner, lines, planes} of an operand in boxes of 64 inner elements x
 // `box` lines x 1 plane, 128-byte swizzle
-bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t K, int box, int planes,
-                 int64_t plane_stride) {
+bool map_operand(CUtensorMap *m, const Operand &o, int64_t rows, int64_t K, int box) {
   const bool km = kmajor(o);
   const int64_t inner = km ? K : rows, lines = km ? rows : K;
-  const int64_t ld = lines == 1 ? (inner + 7) / 8 * 8 : (km ? o.rs : o.ks);
-  return make_map3d(m, o.p, inner, lines, planes, ld, planes == 1 ? ld * lines : plane_stride, box);
+  const int64_t ld = lines == 1 ? pack_ld(inner) : (km ? o.rs : o.ks);
+  const int planes = std::max(1, o.planes);
+  return make_map3d(m, o.p, inner, lines, planes, ld, planes == 1 ? ld * lines : o.plane_stride, box);
 }
+
+// The pairs of planes of an fp32 product, smallest products first
+constexpr uint8_t kPlanePairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
 
 }  // namespace
 
 bool dense_tc_ok(const DenseGemm &g) {
-  if (g.dtype != MOE_BF16 || g.K < 1 || g.M < 1) return false;
-  if (g.M > 0x7ffffe00 || g.K > 0x7ffffe00 || g.N > 0x7ffffe00) return false;
+  if (g.K < 1 || g.M < 1 || g.M > 0x7ffffe00 || g.K > 0x7ffffe00 || g.N > 0x7ffffe00) return false;
+  const int planes = g.dtype == MOE_F32 ? 3 : 0;
   for (const Operand *o : {&g.b, &g.b3, &g.b2})
-    if (o->p && !tma_ok(*o, g.N, g.K)) return false;
+    if (o->p && (!tma_ok(*o, g.N, g.K) || (planes == 3) != (o->planes == 3))) return false;
   for (const Operand *o : {&g.a, &g.a2})
-    if (o->p && !tma_ok(*o, g.M, g.K)) return false;
+    if (o->p && (!tma_ok(*o, g.M, g.K) || (planes == 3) != (o->planes == 3))) return false;
   return (!g.a2.p || (kmajor(g.a) == kmajor(g.a2) && kmajor(g.b) == kmajor(g.b2))) &&
          (!g.b3.p || kmajor(g.b) == kmajor(g.b3)) && (g.epi != kDenseGated || kmajor(g.b));
 }
@@ -692,15 +705,17 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
   for (int p = 0; p < n; ++p) {
     TcProblem &Q = P.pr[p];
     const DenseGemm &G = g[order[p]];
-    bool ok = map_operand(&Q.a[0], G.a, G.M, G.K, kmajor(G.a) ? BM : BK, 1, 0) &&
-              map_operand(&Q.b[0], G.b, G.N, G.K, box_b(G.b), 1, 0);
+    bool ok = map_operand(&Q.a[0], G.a, G.M, G.K, kmajor(G.a) ? BM : BK) &&
+              map_operand(&Q.b[0], G.b, G.N, G.K, box_b(G.b));
     if (G.a2.p)
-      ok = ok && map_operand(&Q.a[1], G.a2, G.M, G.K, kmajor(G.a2) ? BM : BK, 1, 0) &&
-           map_operand(&Q.b[1], G.b2, G.N, G.K, box_b(G.b2), 1, 0);
-    if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, box_b(G.b3), 1, 0);
+      ok = ok && map_operand(&Q.a[1], G.a2, G.M, G.K, kmajor(G.a2) ? BM : BK) &&
+           map_operand(&Q.b[1], G.b2, G.N, G.K, box_b(G.b2));
+    if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, box_b(G.b3));
     if (!ok) return cudaErrorInvalidValue;
-    Q.segs = G.a2.p ? 2 : 1;
-    for (int i = 0; i < Q.segs; ++i) Q.seg[i] = {(uint8_t)i, 0, (uint8_t)i, 0};
+    const int pairs_of_planes = G.dtype == MOE_F32 ? 6 : 1;
+    for (int q = 0; q < pairs_of_planes; ++q)
+      for (uint8_t i = 0; i < (G.a2.p ? 2 : 1); ++i)
+        Q.seg[Q.segs++] = pairs_of_planes == 1 ? Seg{i, 0, i, 0} : Seg{i, kPlanePairs[q][0], i, kPlanePairs[q][1]};
     Q.amn = !kmajor(G.a);
     Q.bmn = !kmajor(G.b);
     Q.M = G.M;
@@ -721,13 +736,7 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
     Q.out2 = G.out2;
     Q.out3 = G.out3;
   }
-  using B = __nv_bfloat16;
-  switch (g[0].epi) {
-    case kDenseLinear: return launch_pair_as<kDenseLinear, B>(P, s);
-    case kDenseGated: return launch_pair_as<kDenseGated, B>(P, s);
-    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, B>(P, s);
-    default: return launch_pair_as<kDenseStore, B>(P, s);
-  }
+  return g[0].dtype == MOE_F32 ? launch_as<float>(g[0].epi, P, s) : launch_as<__nv_bfloat16>(g[0].epi, P, s);
 }
 
 }  // namespace moe
