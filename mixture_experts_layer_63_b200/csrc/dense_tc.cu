@@ -51,6 +51,15 @@ constexpr int kGroupM = DT_GM;                   // row tiles of a raster group
 constexpr int kMaxProblems = 4;
 constexpr int kMaxSegs = 12;
 
+// fp32 products (planes, see dense_pack.cu): the accumulator is read out every
+// chunk of kBks k-blocks and the chunks are added in registers.  The tensor
+// core adds into its accumulator with truncation, about half an ulp of the
+// accumulator lost towards zero an MMA (measured: 2.6e-6 relative after 49 of
+// them); eight MMAs of leading products a chunk keep that below 4e-7 for any
+// K.  The small products come first in a chunk, while the accumulator is small.
+template <typename T>
+constexpr bool kChunked = sizeof(T) == 4;
+
 // A stretch of k-blocks: tensor map and plane (third coordinate) of each operand
 struct Seg {
   uint8_t a, az, b, bz;
@@ -364,6 +373,31 @@ struct Epilogue {
   }
 };
 
+// 32 accumulator columns back into this thread's TMEM lane
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Accumulator column of a warp's group i of 32 (its half of the output
+// columns; gated: of the gate's, then of the up-projection's); -1: none
+template <int EPI>
+__device__ __forceinline__ int group_col(const TcParams &P, int half, int i) {
+  const int w = P.bnh / 2, g = EPI == kDenseGated ? i >> 1 : 0, c = 32 * (EPI == kDenseGated ? i & 1 : i);
+  return c < w ? g * P.bnh + half * w + c : -1;
+}
+
 // --------------------------------- the kernel ----------------------------------
 template <int EPI, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -430,15 +464,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     const uint32_t smem0 = smem_u32(smem), fb0 = smem_u32(full_bar) & 0xFEFFFFFFu;      // the even CTA's barriers
     const bool wide = P.bn == 256;
-    // k-blocks [0, KB) of one segment; the operand orders are constants of the
+    // k-blocks [kb, kb1) of one segment; the operand orders are constants of the
     // loop (a stage has to be refilled within the time of one stage's MMAs)
-    auto fill = [&](auto amn, auto bmn, const CUtensorMap *ma, const CUtensorMap *mb, int am, int bn0, int KB,
-                    Seg S) -> bool {
-      for (int kb = 0; kb < KB; kb += kBks) {
+    auto fill = [&](auto amn, auto bmn, const CUtensorMap *ma, const CUtensorMap *mb, int am, int bn0, int kb,
+                    int kb1, Seg S) -> bool {
+      for (; kb < kb1; kb += kBks) {
         if (!mbar_wait(&empty_bar[stage], phase ^ 1u, &s_abort, P.err, s_limit)) return false;
         uint32_t sa = smem0 + (uint32_t)stage * stage_bytes, sb = sa + kBks * kABytes;
         const uint32_t fb = fb0 + 8 * stage;
-        const int nq = min(kBks, KB - kb);
+        const int nq = min(kBks, kb1 - kb);
         if (rank == 0) {
           mbar_expect_tx(&full_bar[stage], 2 * nq * (kABytes + b_bytes));
           armed |= 1u << stage;
@@ -474,16 +508,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int am = q.m * 2 * BM + (int)rank * BM;
       // gated: the even CTA stages rows of W1, the odd one the same rows of W3
       const int bn0 = q.n * P.bnh + (EPI == kDenseGated ? 0 : (int)rank * (P.bn / 2));
-      for (int sg = 0; ok && sg < Q.segs; ++sg) {
-        const Seg S = Q.seg[sg];
-        const CUtensorMap *ma = &Q.a[S.a];
-        const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
-        if (Q.amn) {
-          ok = Q.bmn ? fill(IntC<1>{}, IntC<1>{}, ma, mb, am, bn0, Q.KB, S)
-                     : fill(IntC<1>{}, IntC<0>{}, ma, mb, am, bn0, Q.KB, S);
-        } else {
-          ok = Q.bmn ? fill(IntC<0>{}, IntC<1>{}, ma, mb, am, bn0, Q.KB, S)
-                     : fill(IntC<0>{}, IntC<0>{}, ma, mb, am, bn0, Q.KB, S);
+      const int chunk = kChunked<T> ? kBks : Q.KB;
+      for (int kb = 0; ok && kb < Q.KB; kb += chunk) {
+        const int kb1 = min(Q.KB, kb + chunk);
+        for (int sg = 0; ok && sg < Q.segs; ++sg) {
+          const Seg S = Q.seg[sg];
+          const CUtensorMap *ma = &Q.a[S.a];
+          const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
+          if (Q.amn) {
+            ok = Q.bmn ? fill(IntC<1>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
+                       : fill(IntC<1>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
+          } else {
+            ok = Q.bmn ? fill(IntC<0>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
+                       : fill(IntC<0>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
+          }
         }
       }
     }
@@ -507,32 +545,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t adesc = amn ? mn128_desc(smem0) : sw128_desc(smem0);
       const uint64_t bdesc = bmn ? mn128_desc(smem0 + kBks * kABytes) : sw128_desc(smem0 + kBks * kABytes);
       const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
-      if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
-      uint32_t accum = 0;
-      for (int sg = 0; ok && sg < segs; ++sg) {
-        for (int kb = 0; kb < KB; kb += kBks) {
-          if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
-          tc_fence_after();
-          uint64_t ad = adesc + (uint32_t)stage * (stage_bytes >> 4), bd = bdesc + (uint32_t)stage * (stage_bytes >> 4);
-          const int nq = min(kBks, KB - kb);
-          for (int q2 = 0; q2 < nq; ++q2) {
+      const int chunk = kChunked<T> ? kBks : KB;
+      for (int kc = 0; ok && kc < KB; kc += chunk) {
+        if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
+        const int kc1 = min(KB, kc + chunk);
+        uint32_t accum = 0;
+        for (int sg = 0; ok && sg < segs; ++sg) {
+          for (int kb = kc; kb < kc1; kb += kBks) {
+            if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
+            tc_fence_after();
+            uint64_t ad = adesc + (uint32_t)stage * (stage_bytes >> 4), bd = bdesc + (uint32_t)stage * (stage_bytes >> 4);
+            const int nq = min(kBks, kc1 - kb);
+            for (int q2 = 0; q2 < nq; ++q2) {
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k) {
-              umma_bf16_pair(d_tmem, ad + k * astep, bd + k * bstep, idesc, accum);
-              accum = 1;
+              for (int k = 0; k < BK / 16; ++k) {
+                umma_bf16_pair(d_tmem, ad + k * astep, bd + k * bstep, idesc, accum);
+                accum = 1;
+              }
+              ad += kABytes >> 4;
+              bd += b_bytes >> 4;
             }
-            ad += kABytes >> 4;
-            bd += b_bytes >> 4;
+            umma_commit_pair_both(&empty_bar[stage]);
+            if (++stage == kStages) { stage = 0; phase ^= 1u; }
           }
-          umma_commit_pair_both(&empty_bar[stage]);
-          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
+        if (!ok) break;
+        umma_commit_pair_both(&accf_bar[acc]);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      if (!ok) break;
-      umma_commit_pair_both(&accf_bar[acc]);
-      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
     umma_commit_pair_local(&drain_bar);
     mbar_wait_drain(&drain_bar, 0);
@@ -564,10 +606,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       Epilogue<EPI, T> ep(P, Q, (int64_t)q.m * 2 * BM + rank * BM + quarter * 32, col0, half * w, half * w + w, stg,
                           lane);
-      ep.begin();
-      if (!__all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit))) break;
-      tc_fence_after();
-      ep.run(tmem_base + (uint32_t)(acc * kAccCols) + ((uint32_t)(quarter * 32) << 16), sb);
+      const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+      if (!kChunked<T>) ep.begin();
+      bool ok = true;
+      if (kChunked<T>) {
+        // all chunks but the last join the sum in registers; the last one's
+        // place in TMEM then takes the whole sum
+        float sum[4][32] = {};
+        const int chunks = (Q.KB + kBks - 1) / kBks;
+        for (int c = 0; c < chunks; ++c) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit)))) break;
+          tc_fence_after();
+          const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int col = group_col<EPI>(P, half, i);
+            if (col < 0) continue;
+            uint32_t r[32];
+            tmem_ld32(ta + col, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(r[j]);
+            if (c + 1 == chunks) tmem_st32(ta + col, sum[i]);
+          }
+          if (c + 1 == chunks) break;
+          tc_fence_before();
+          mbar_arrive_cluster(acce_even[acc]);
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+        if (ok) {
+          tmem_st_wait();
+          ep.begin();
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit));
+        tc_fence_after();
+      }
+      if (!ok) break;
+      ep.run(tmem_base + (uint32_t)(acc * kAccCols) + lanes, sb);
       __syncwarp();
       tc_fence_before();
       mbar_arrive_cluster(acce_even[acc]);
