@@ -110,7 +110,7 @@ size_t pack_room(int dtype, int64_t lines, int64_t inner, int64_t ld) {
 }
 
 struct LinearLayout {
-  size_t dz, part, pack, total;
+  size_t dz, part, tail, pack, total;
 };
 
 LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
@@ -123,6 +123,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
     L.part = t.take(colsum_scratch(c.M, c.N, 1));
     room += pack_room(c.dtype, c.M, c.N, act ? pack_ld(c.N) : c.ld_y);
   }
+  L.tail = t.take(dense_tail_bytes());
   L.pack = t.take(room);
   L.total = t.o;
   return L;
@@ -133,8 +134,8 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
 // later groups of the call.
 class Products {
  public:
-  Products(int dtype, void *ws, size_t pack, size_t end, cudaStream_t s)
-      : dtype_(dtype), base_(static_cast<char *>(ws)), at_(pack), end_(end), s_(s) {}
+  Products(int dtype, void *ws, size_t tail, size_t pack, size_t end, cudaStream_t s)
+      : dtype_(dtype), base_(static_cast<char *>(ws)), tail_(tail), at_(pack), end_(end), s_(s) {}
 
   cudaError_t run(DenseGemm *g, int n) {
     uint32_t *err = reinterpret_cast<uint32_t *>(base_);
@@ -156,7 +157,7 @@ class Products {
         launched_ = jobs_;
         if (e != cudaSuccess) return e;
         if (n == 1 && dense_few_ok(q[0])) return launch_dense_few(q[0], err, s_);
-        return launch_dense_tc(q, n, err, s_);
+        return launch_dense_tc(q, n, err, reinterpret_cast<float *>(base_ + tail_), s_);
       }
       jobs_ = launched_;
     }
@@ -199,7 +200,7 @@ class Products {
 
   int dtype_;
   char *base_;
-  size_t at_, end_;
+  size_t tail_, at_, end_;
   cudaStream_t s_;
   PackJob job_[kMaxJobs];
   int jobs_ = 0, launched_ = 0;
@@ -238,7 +239,7 @@ moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *
 }
 
 struct GatedLayout {
-  size_t h, da, du, part, pack, total;
+  size_t h, da, du, part, tail, pack, total;
 };
 
 GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
@@ -256,6 +257,7 @@ GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
     L.part = t.take(colsum_scratch(T, std::max(c.d_ff, c.d_model), 3));
     pack += 2 * room(T, f, ldh) + room(T, d, c.ld_y);
   }
+  L.tail = t.take(dense_tail_bytes());
   L.pack = t.take(pack);
   L.total = t.o;
   return L;
@@ -307,7 +309,7 @@ moe_status moe_linear(const moe_linear_config *cfg, const void *x, const void *w
   g.out = y;
   g.ld_o = c.ld_y;
   g.pre = z;
-  Products run(c.dtype, ws, L.pack, L.total, reinterpret_cast<cudaStream_t>(stream));
+  Products run(c.dtype, ws, L.tail, L.pack, L.total, reinterpret_cast<cudaStream_t>(stream));
   return dense_status(run.run(g));
 }
 
@@ -343,7 +345,7 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
   int n = 0;
   if (dx && c.M > 0) g[n++] = product(c.dtype, c.M, c.N, c.K, dz, {w, 1, c.ld_w}, dx, c.ld_x);
   if (dw) g[n++] = product(c.dtype, c.N, c.M, c.K, {dz.p, 1, dz.rs}, {x, 1, c.ld_x}, dw, c.K);
-  Products run(c.dtype, ws, L.pack, L.total, s);
+  Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
   if (e == cudaSuccess && n > 0) e = run.run(g, n);
   return dense_status(e);
 }
@@ -395,7 +397,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   g.ld_o = ldh;
   g.pre = a;
   g.pre3 = u;
-  Products run(c.dtype, ws, L.pack, L.total, s);
+  Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
   cudaError_t e = run.run(g);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   DenseGemm q{};
@@ -443,7 +445,7 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   char *h = base + L.h, *da = base + L.da, *du = base + L.du;
   float *part = reinterpret_cast<float *>(base + L.part);
   cudaError_t e = cudaSuccess;
-  Products run(c.dtype, ws, L.pack, L.total, s);
+  Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
   if (hidden && T > 0) {
     DenseGemm g{};
     g.epi = kDenseGatedGrad;

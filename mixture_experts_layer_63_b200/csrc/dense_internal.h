@@ -55,7 +55,10 @@ cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s);
 // bf16 planes) with base and lines 16-byte aligned.  launch_dense_tc runs up
 // to four products with one epilogue in one launch.
 bool dense_tc_ok(const DenseGemm &g);
-cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s);
+// err: the workspace's control block; part: dense_tail_bytes() of scratch for
+// tiles that are cut between CTA pairs.
+size_t dense_tail_bytes();
+cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *part, cudaStream_t s);
 
 // Copies of matrices for the tensor cores (dense_pack.cu): `lines` lines of
 // `inner` elements, ld apart, into bf16 planes of round_up(inner, 8) elements a

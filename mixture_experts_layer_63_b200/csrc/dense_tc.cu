@@ -79,6 +79,12 @@ struct TcProblem {
 
 struct TcParams {
   TcProblem pr[kMaxProblems];
+  // the shared tail: tiles from dp_tiles on are cut into steps (below), laid
+  // end to end and split evenly over `workers` pairs.  Problem p's tail tiles
+  // are [tail_tile[p], tile_end), their steps [tail_step[p], tail_step[p+1])
+  int32_t dp_tiles, workers, tail_tile[kMaxProblems];
+  int64_t tail_step[kMaxProblems + 1];
+  float *part;                   // partial tiles, two slots a worker
   int32_t nprob, act;
   int32_t bn, bnh;               // accumulator columns; output columns of a tile
   uint32_t *err;
@@ -104,24 +110,89 @@ __device__ __forceinline__ void tma_load_3d_at(uint32_t dst, const CUtensorMap *
 }
 
 struct TilePos {
-  int p, m, n;
+  int m, n;
 };
 
-// Raster order: groups of kGroupM row tiles, columns outer within a group, so
-// that the pairs at work share few row and column panels in L2.
-__device__ __forceinline__ TilePos tile_pos(const TcParams &P, int t) {
-  TilePos r;
-  r.p = 0;
-  int first = 0;
-  while (r.p + 1 < P.nprob && t >= P.pr[r.p].tile_end) first = P.pr[r.p++].tile_end;
+// Raster order within a problem: groups of kGroupM row tiles, columns outer
+// within a group, so that the pairs at work share few row and column panels
+// in L2.
+__device__ __forceinline__ TilePos tile_pos(const TcParams &P, int p, int t) {
+  const int first = p ? P.pr[p - 1].tile_end : 0;
   t -= first;
-  const int tm = P.pr[r.p].tiles_m, tn = (P.pr[r.p].tile_end - first) / tm;
+  const int tm = P.pr[p].tiles_m, tn = (P.pr[p].tile_end - first) / tm;
   const int g = t / (kGroupM * tn), in = t - g * kGroupM * tn;
   const int gm = min(kGroupM, tm - g * kGroupM);
-  r.m = g * kGroupM + in % gm;
-  r.n = in / gm;
-  return r;
+  return {g * kGroupM + in % gm, in / gm};
 }
+
+// ----------------------------------- work ---------------------------------------
+// A tile's steps are the fills of its ring stages: kBks k-blocks of one
+// segment.  bf16: segment by segment; fp32 (chunked): k-block pair by pair, all
+// segments of each.  A pair's work: whole tiles of the full waves, dealt
+// round-robin, then its share of the tail.  A tile cut between pairs is summed
+// by whichever of its pieces is finished last, in the pieces' order: nobody
+// ever waits for another pair, and the result does not depend on which it was.
+struct Piece {
+  int tile, p;                   // p: its problem
+  int s0, s1, steps;             // steps [s0, s1) of the tile's
+  int index, count;              // this piece among the tile's
+  int slot;                      // partial tile of this piece (worker * 2 + 0 / 1)
+  int first_worker, tail;        // worker of piece 0; tile's number in the tail
+  __device__ __forceinline__ bool whole() const { return count == 1; }
+};
+
+template <typename T>
+__device__ __forceinline__ int steps_of(const TcProblem &Q) {
+  return (Q.KB + kBks - 1) / kBks * Q.segs;
+}
+
+template <typename T>
+struct Work {
+  const TcParams &P;
+  const int pair, npairs;
+  int t;
+  int64_t x, x1;                 // what is left of the tail share
+  __device__ Work(const TcParams &p, int pair_, int npairs_) : P(p), pair(pair_), npairs(npairs_), t(pair_) {
+    const int64_t R = p.tail_step[p.nprob];
+    x = pair < p.workers ? R * pair / p.workers : 0;
+    x1 = pair < p.workers ? R * (pair + 1) / p.workers : 0;
+  }
+  // the worker whose share holds step y
+  __device__ __forceinline__ int owner(int64_t y) const {
+    return (int)(((y + 1) * P.workers - 1) / P.tail_step[P.nprob]);
+  }
+  __device__ __forceinline__ bool next(Piece &q) {
+    if (t < P.dp_tiles) {
+      q.tile = t;
+      q.p = 0;
+      while (q.p + 1 < P.nprob && t >= P.pr[q.p].tile_end) ++q.p;
+      q.steps = steps_of<T>(P.pr[q.p]);
+      q.s0 = 0;
+      q.s1 = q.steps;
+      q.index = 0;
+      q.count = 1;
+      t += npairs;
+      return true;
+    }
+    if (x >= x1) return false;
+    q.p = 0;
+    while (x >= P.tail_step[q.p + 1]) ++q.p;
+    q.steps = steps_of<T>(P.pr[q.p]);
+    const int64_t in = x - P.tail_step[q.p];
+    const int k = (int)(in / q.steps);
+    const int64_t begin = P.tail_step[q.p] + (int64_t)k * q.steps;      // the tile's first step
+    q.tile = P.tail_tile[q.p] + k;
+    q.s0 = (int)(x - begin);
+    q.s1 = (int)min((int64_t)q.steps, x1 - begin);
+    q.first_worker = owner(begin);
+    q.index = pair - q.first_worker;
+    q.count = owner(begin + q.steps - 1) - q.first_worker + 1;
+    q.slot = 2 * pair + (q.index == 0 ? 1 : 0);
+    q.tail = q.tile - P.dp_tiles;
+    x = begin + q.s1;
+    return true;
+  }
+};
 
 // ------------------------------- epilogue pieces --------------------------------
 // A warp moves its 32 rows in chunks of CW columns (64 bytes of a row: four
@@ -398,6 +469,72 @@ __device__ __forceinline__ int group_col(const TcParams &P, int half, int i) {
   return c < w ? g * P.bnh + half * w + c : -1;
 }
 
+// A piece that is not the whole tile: this warp's part of the accumulator to
+// the piece's slot, then a count of the pieces that are there.  The warp that
+// finds itself last adds the tile's pieces in order, puts the sum in TMEM and
+// returns true.  A field of four bits a warp counts its pieces (at most
+// kMaxPieces) and is back at zero afterwards, for the next launch.
+constexpr int kMaxPieces = 14;
+constexpr size_t kTailCountOffset = 1024;             // into the workspace's control block
+constexpr int kMaxTail = 320;                         // tiles of the tail at most
+constexpr int64_t kSlotFloats = 2 * BM * kAccCols;    // a pair's accumulators
+static_assert(kTailCountOffset + 4 * 2 * kMaxTail <= kCtrlBytes, "counters of the tail");
+
+template <int EPI>
+__device__ bool join_pieces(const TcParams &P, const Piece &pc, uint32_t ta, int rank, int ew, int half, int lane) {
+  auto at = [&](int slot) {
+    return reinterpret_cast<float4 *>(P.part + slot * kSlotFloats) + (rank * kEpiWarps + ew) * (4 * 8 * 32) + lane;
+  };
+  float4 *mine = at(pc.slot);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = group_col<EPI>(P, half, i);
+    if (col < 0) continue;
+    uint32_t r[32];
+    tmem_ld32(ta + col, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      __stcg(mine + (i * 8 + j) * 32, make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                  __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+  }
+  __threadfence();
+  __syncwarp();
+  uint32_t *count = P.err + kTailCountOffset / 4 + pc.tail * 2 + rank;
+  int last = 0;
+  if (lane == 0) {
+    const uint32_t old = atomicAdd(count, 1u << (4 * ew));
+    last = (int)((old >> (4 * ew)) & 15u) == pc.count - 1;
+    if (last) atomicSub(count, (uint32_t)pc.count << (4 * ew));
+  }
+  last = __shfl_sync(0xffffffffu, last, 0);
+  if (!last) return false;
+  __threadfence();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = group_col<EPI>(P, half, i);
+    if (col < 0) continue;
+    float v[32];
+    for (int k = 0; k < pc.count; ++k) {
+      // piece 0 is the end of its worker's share, the others begin theirs
+      const float4 *src = at(2 * (pc.first_worker + k) + (k == 0 ? 1 : 0)) + i * 8 * 32;
+      float4 f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __ldcg(src + j * 32);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[4 * j] = k ? v[4 * j] + f[j].x : f[j].x;
+        v[4 * j + 1] = k ? v[4 * j + 1] + f[j].y : f[j].y;
+        v[4 * j + 2] = k ? v[4 * j + 2] + f[j].z : f[j].z;
+        v[4 * j + 3] = k ? v[4 * j + 3] + f[j].w : f[j].w;
+      }
+    }
+    tmem_st32(ta + col, v);
+  }
+  tmem_st_wait();
+  return true;
+}
+
 // --------------------------------- the kernel ----------------------------------
 template <int EPI, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -419,7 +556,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int tiles = P.pr[P.nprob - 1].tile_end;
 
   if (tid == 32) {
     for (int st = 0; st < kStages; ++st) {
@@ -502,26 +638,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return true;
     };
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += npairs) {
-      const TilePos q = tile_pos(P, t);
-      const TcProblem &Q = P.pr[q.p];
+    Work<T> work(P, pair, npairs);
+    Piece w;
+    while (ok && work.next(w)) {
+      const TilePos q = tile_pos(P, w.p, w.tile);
+      const TcProblem &Q = P.pr[w.p];
       const int am = q.m * 2 * BM + (int)rank * BM;
       // gated: the even CTA stages rows of W1, the odd one the same rows of W3
       const int bn0 = q.n * P.bnh + (EPI == kDenseGated ? 0 : (int)rank * (P.bn / 2));
-      const int chunk = kChunked<T> ? kBks : Q.KB;
-      for (int kb = 0; ok && kb < Q.KB; kb += chunk) {
-        const int kb1 = min(Q.KB, kb + chunk);
-        for (int sg = 0; ok && sg < Q.segs; ++sg) {
-          const Seg S = Q.seg[sg];
-          const CUtensorMap *ma = &Q.a[S.a];
-          const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
-          if (Q.amn) {
-            ok = Q.bmn ? fill(IntC<1>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
-                       : fill(IntC<1>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
-          } else {
-            ok = Q.bmn ? fill(IntC<0>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
-                       : fill(IntC<0>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
-          }
+      // runs of steps in one segment
+      const int per = kChunked<T> ? 1 : w.steps / Q.segs;
+      for (int st = w.s0, run; ok && st < w.s1; st += run) {
+        const int sg = kChunked<T> ? st % Q.segs : st / per;
+        const int i = kChunked<T> ? st / Q.segs : st - sg * per;
+        run = kChunked<T> ? 1 : min(per - i, w.s1 - st);
+        const int kb = i * kBks, kb1 = min(Q.KB, (i + run) * kBks);
+        const Seg S = Q.seg[sg];
+        const CUtensorMap *ma = &Q.a[S.a];
+        const CUtensorMap *mb = &Q.b[EPI == kDenseGated ? (int)rank : S.b];
+        if (Q.amn) {
+          ok = Q.bmn ? fill(IntC<1>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
+                     : fill(IntC<1>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
+        } else {
+          ok = Q.bmn ? fill(IntC<0>{}, IntC<1>{}, ma, mb, am, bn0, kb, kb1, S)
+                     : fill(IntC<0>{}, IntC<0>{}, ma, mb, am, bn0, kb, kb1, S);
         }
       }
     }
@@ -536,40 +676,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int stage = 0, acc = 0;
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
-    for (int t = pair; ok && t < tiles; t += npairs) {
-      const TcProblem &Q = P.pr[tile_pos(P, t).p];
-      const int KB = Q.KB, segs = Q.segs;
+    Work<T> work(P, pair, npairs);
+    Piece w;
+    while (ok && work.next(w)) {
+      const TcProblem &Q = P.pr[w.p];
+      const int KB = Q.KB, segs = Q.segs, per = kChunked<T> ? segs : w.steps / segs;
       const bool amn = Q.amn, bmn = Q.bmn;
       const uint32_t idesc = idesc_bf16(2 * BM, P.bn) | (amn ? 1u << 15 : 0u) | (bmn ? 1u << 16 : 0u);
       // descriptors of stage 0; the address field counts 16 bytes
       const uint64_t adesc = amn ? mn128_desc(smem0) : sw128_desc(smem0);
       const uint64_t bdesc = bmn ? mn128_desc(smem0 + kBks * kABytes) : sw128_desc(smem0 + kBks * kABytes);
       const uint32_t astep = amn ? 2048 >> 4 : 32 >> 4, bstep = bmn ? 2048 >> 4 : 32 >> 4;
-      const int chunk = kChunked<T> ? kBks : KB;
-      for (int kc = 0; ok && kc < KB; kc += chunk) {
+      // one accumulator a piece (fp32: a chunk of it)
+      for (int st = w.s0; ok && st < w.s1;) {
         if (!mbar_wait<true>(&acce_bar[acc], acc_phase ^ 1u, &s_abort, P.err, s_limit)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kAccCols);
-        const int kc1 = min(KB, kc + chunk);
+        const int end = kChunked<T> ? min(w.s1, st - st % segs + segs) : w.s1;
+        int i = kChunked<T> ? st / segs : st % per;          // step within its segment
         uint32_t accum = 0;
-        for (int sg = 0; ok && sg < segs; ++sg) {
-          for (int kb = kc; kb < kc1; kb += kBks) {
-            if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
-            tc_fence_after();
-            uint64_t ad = adesc + (uint32_t)stage * (stage_bytes >> 4), bd = bdesc + (uint32_t)stage * (stage_bytes >> 4);
-            const int nq = min(kBks, kc1 - kb);
-            for (int q2 = 0; q2 < nq; ++q2) {
+        for (; st < end; ++st) {
+          if (!mbar_wait<true>(&full_bar[stage], phase, &s_abort, P.err, s_limit)) { ok = false; break; }
+          tc_fence_after();
+          uint64_t ad = adesc + (uint32_t)stage * (stage_bytes >> 4), bd = bdesc + (uint32_t)stage * (stage_bytes >> 4);
+          const int nq = min(kBks, KB - i * kBks);
+          for (int q2 = 0; q2 < nq; ++q2) {
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k) {
-                umma_bf16_pair(d_tmem, ad + k * astep, bd + k * bstep, idesc, accum);
-                accum = 1;
-              }
-              ad += kABytes >> 4;
-              bd += b_bytes >> 4;
+            for (int k = 0; k < BK / 16; ++k) {
+              umma_bf16_pair(d_tmem, ad + k * astep, bd + k * bstep, idesc, accum);
+              accum = 1;
             }
-            umma_commit_pair_both(&empty_bar[stage]);
-            if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            ad += kABytes >> 4;
+            bd += b_bytes >> 4;
           }
+          umma_commit_pair_both(&empty_bar[stage]);
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
+          if (!kChunked<T> && ++i == per) i = 0;
         }
         if (!ok) break;
         umma_commit_pair_both(&accf_bar[acc]);
@@ -591,9 +733,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float *sb = s_bias[ew];
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = pair; t < tiles; t += npairs) {
-      const TilePos q = tile_pos(P, t);
-      const TcProblem &Q = P.pr[q.p];
+    Work<T> work(P, pair, npairs);
+    Piece pc;
+    while (work.next(pc)) {
+      const TilePos q = tile_pos(P, pc.p, pc.tile);
+      const TcProblem &Q = P.pr[pc.p];
       const int col0 = q.n * P.bnh, w = P.bnh / 2;
       if ((EPI == kDenseLinear || EPI == kDenseGated) && Q.bias) {
         for (int i = lane; i < w; i += 32) {
@@ -607,13 +751,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Epilogue<EPI, T> ep(P, Q, (int64_t)q.m * 2 * BM + rank * BM + quarter * 32, col0, half * w, half * w + w, stg,
                           lane);
       const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-      if (!kChunked<T>) ep.begin();
+      if (!kChunked<T> && pc.whole()) ep.begin();
       bool ok = true;
       if (kChunked<T>) {
         // all chunks but the last join the sum in registers; the last one's
         // place in TMEM then takes the whole sum
         float sum[4][32] = {};
-        const int chunks = (Q.KB + kBks - 1) / kBks;
+        const int chunks = (pc.s1 - 1) / Q.segs - pc.s0 / Q.segs + 1;
         for (int c = 0; c < chunks; ++c) {
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit)))) break;
           tc_fence_after();
@@ -636,14 +780,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (ok) {
           tmem_st_wait();
-          ep.begin();
+          if (pc.whole()) ep.begin();
         }
       } else {
         ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit));
         tc_fence_after();
       }
       if (!ok) break;
-      ep.run(tmem_base + (uint32_t)(acc * kAccCols) + lanes, sb);
+      const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
+      bool finish = true;
+      if (!pc.whole()) {
+        finish = join_pieces<EPI>(P, pc, ta, (int)rank, ew, half, lane);
+        if (finish) ep.begin();
+      }
+      if (finish) ep.run(ta, sb);
       __syncwarp();
       tc_fence_before();
       mbar_arrive_cluster(acce_even[acc]);
@@ -660,6 +810,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ------------------------------- host side --------------------------------------
 constexpr int kMaxDevices = 64;
+constexpr int kMaxPairs = 80;           // pairs of a launch at most (slots of the workspace)
+#ifndef DT_JOIN
+#define DT_JOIN 10
+#endif
+#ifndef DT_MIN
+#define DT_MIN 4
+#endif
+constexpr int kJoinSteps = DT_JOIN, kMinSteps = DT_MIN;
 
 // As many CTA pairs as fit at once.  The attribute is set and the occupancy
 // asked once a device (a second thread that asks meanwhile gets the same).
@@ -694,18 +852,50 @@ cudaError_t pairs_of(size_t smem, int *pairs) {
 }
 
 template <int EPI, typename T>
-cudaError_t launch_pair_as(const TcParams &P, cudaStream_t s) {
+cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
   constexpr auto kern = dense_pair_kernel<EPI, T>;
   constexpr size_t smem = 1024 + kStages * kBks * (kABytes + 128 * BK * 2) +
                           kEpiWarps * Epilogue<EPI, T>::kIn * kStgBytes;
   int pairs = 0;
   const cudaError_t e = pairs_of<kern>(smem, &pairs);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, 2 * (unsigned)std::min<int>(pairs, P.pr[P.nprob - 1].tile_end), kThreads, smem, s, P);
+  pairs = std::min(pairs, kMaxPairs);
+  // The tail: the tiles behind the last full wave, when spreading them over
+  // all pairs saves more than joining their pieces costs.  A plain last wave
+  // takes a tile's steps; spread, the share of it that the tail fills, plus
+  // about kJoinSteps for the partial tiles' way through L2.
+  const int tiles = P.pr[P.nprob - 1].tile_end, last = tiles % pairs;
+  P.dp_tiles = tiles;
+  P.workers = 0;
+  if (last > 0 && P.part) {
+    const int dp = tiles - last;
+    int64_t total = 0;
+    int deepest = 0;
+    for (int p = 0; p < P.nprob; ++p) {
+      const int begin = std::max(dp, p ? P.pr[p - 1].tile_end : 0), n = std::max(0, P.pr[p].tile_end - begin);
+      const int steps = (P.pr[p].KB + kBks - 1) / kBks * P.pr[p].segs;
+      P.tail_tile[p] = begin;
+      P.tail_step[p] = total;
+      total += (int64_t)n * steps;
+      if (n) deepest = std::max(deepest, steps);
+    }
+    P.tail_step[P.nprob] = total;
+    // at least kMinSteps a worker, at most kMaxPieces pieces a tile
+    const int64_t least = std::max<int64_t>(kMinSteps, (deepest + kMaxPieces - 3) / (kMaxPieces - 2));
+    const int workers = (int)std::min<int64_t>(pairs, total / least);
+    if (workers > last && (double)total / workers + kJoinSteps < deepest) {
+      P.dp_tiles = dp;
+      P.workers = workers;
+    }
+  }
+  if (P.workers == 0)
+    for (int p = 0; p <= P.nprob; ++p) P.tail_step[p] = 0;
+  const int grid = std::min(pairs, std::max(P.dp_tiles, P.workers));
+  return launch_kernel(kern, 2 * (unsigned)grid, kThreads, smem, s, P);
 }
 
 template <typename T>
-cudaError_t launch_as(int epi, const TcParams &P, cudaStream_t s) {
+cudaError_t launch_as(int epi, TcParams &P, cudaStream_t s) {
   switch (epi) {
     case kDenseLinear: return launch_pair_as<kDenseLinear, T>(P, s);
     case kDenseGated: return launch_pair_as<kDenseGated, T>(P, s);
@@ -749,16 +939,18 @@ bool dense_tc_ok(const DenseGemm &g) {
          (!g.b3.p || kmajor(g.b) == kmajor(g.b3)) && (g.epi != kDenseGated || kmajor(g.b));
 }
 
-cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream_t s) {
+size_t dense_tail_bytes() { return (size_t)kMaxPairs * 2 * kSlotFloats * 4; }
+
+cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *part, cudaStream_t s) {
   if (n < 1 || n > kMaxProblems) return cudaErrorInvalidValue;
   TcParams P{};
   P.err = err;
+  P.part = part;
   P.act = g[0].act;
   P.nprob = n;
-  // columns of a tile: the width whose last wave wastes less (a 128-column
-  // tile costs about 0.55 of a 256-column one)
+  // columns of a tile: 128 where that saves more than its dearer product (a
+  // 128-column tile costs about 0.55 of a 256-column one)
   const bool gated = g[0].epi == kDenseGated;
-  const int pairs = std::max(1, device_sms() / 2);
   auto tiles_of = [&](const DenseGemm &q, int bn) {
     const int w = gated ? bn / 2 : bn;
     return ((q.M + 2 * BM - 1) / (2 * BM)) * ((q.N + w - 1) / w);
@@ -768,8 +960,7 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, cudaStream
     for (int p = 0; p < n; ++p) t += tiles_of(g[p], bn);
     return t;
   };
-  auto cost = [&](int bn) { return (double)((tiles_at(bn) + pairs - 1) / pairs) * (bn == 256 ? 1.0 : 0.55); };
-  P.bn = cost(128) < cost(256) ? 128 : 256;
+  P.bn = 0.55 * (double)tiles_at(128) < (double)tiles_at(256) ? 128 : 256;
   P.bnh = gated ? P.bn / 2 : P.bn;
   if (tiles_at(P.bn) > 0x3fffffff) return cudaErrorInvalidValue;
   auto box_b = [&](const Operand &o) { return kmajor(o) ? P.bn / 2 : BK; };

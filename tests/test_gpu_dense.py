@@ -116,6 +116,17 @@ def test_linear(M, K, N, dtype):
     linear_case(M, K, N, acts[(i + 1) % 5], dtype, bias=False, res=False, save=False, seed=M + N)
 
 
+# long contractions over few tiles: tiles cut into pieces between CTA pairs
+LONG = [(150, 8192, 130), (300, 16384, 520), (700, 4104, 1000), (130, 20000, 24), (2100, 2048, 2304)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,K,N", LONG)
+def test_linear_long_contractions(M, K, N, dtype):
+    for again in range(2):                     # the counters are back at zero
+        linear_case(M, K, N, "gelu_tanh", dtype, bias=True, res=True, save=True, seed=K + again)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("act", list(api.DENSE_ACTS))
 @pytest.mark.parametrize("bias,res,save", [(0, 0, 0), (1, 0, 1), (0, 1, 0), (1, 1, 1)])
@@ -206,6 +217,12 @@ def linear_backward_case(M, K, N, act, dtype, pad=0, seed=0, want=(1, 1, 1)):
 def test_linear_backward(M, K, N, dtype):
     acts = list(api.DENSE_ACTS)
     linear_backward_case(M, K, N, acts[(M + N) % 5], dtype, seed=M)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,K,N", [(8192, 130, 300), (20000, 64, 24), (5000, 520, 264), (300, 256, 9000)])
+def test_linear_backward_long_contractions(M, K, N, dtype):
+    linear_backward_case(M, K, N, "silu", dtype, seed=M)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -353,6 +370,13 @@ def gated_backward_case(T, K, f, act, dtype, bias, pad=0, seed=0, drop=()):
 @pytest.mark.parametrize("T,K,f", GATED)
 def test_gated_backward(T, K, f, dtype):
     gated_backward_case(T, K, f, list(api.DENSE_ACTS)[(T + f) % 5], dtype, True, seed=T)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,K,f", [(300, 4096, 200), (700, 2056, 1000), (4000, 136, 72), (200, 520, 6000)])
+def test_gated_long_contractions(T, K, f, dtype):
+    gated_case(T, K, f, "silu", dtype, True, True, True, seed=T)
+    gated_backward_case(T, K, f, "gelu", dtype, True, seed=T)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
