@@ -514,19 +514,28 @@ __device__ bool join_pieces(const TcParams &P, const Piece &pc, uint32_t ta, int
   for (int i = 0; i < 4; ++i) {
     const int col = group_col<EPI>(P, half, i);
     if (col < 0) continue;
-    float v[32];
-    for (int k = 0; k < pc.count; ++k) {
-      // piece 0 is the end of its worker's share, the others begin theirs
-      const float4 *src = at(2 * (pc.first_worker + k) + (k == 0 ? 1 : 0)) + i * 8 * 32;
-      float4 f[8];
+    // two pieces in flight
+    float v[32] = {};
+    for (int k = 0; k < pc.count; k += 2) {
+      float4 f[2][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __ldcg(src + j * 32);
+      for (int h = 0; h < 2; ++h) {
+        if (k + h >= pc.count) break;
+        // piece 0 is the end of its worker's share, the others begin theirs
+        const float4 *src = at(2 * (pc.first_worker + k + h) + (k + h == 0 ? 1 : 0)) + i * 8 * 32;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[4 * j] = k ? v[4 * j] + f[j].x : f[j].x;
-        v[4 * j + 1] = k ? v[4 * j + 1] + f[j].y : f[j].y;
-        v[4 * j + 2] = k ? v[4 * j + 2] + f[j].z : f[j].z;
-        v[4 * j + 3] = k ? v[4 * j + 3] + f[j].w : f[j].w;
+        for (int j = 0; j < 8; ++j) f[h][j] = __ldcg(src + j * 32);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (k + h >= pc.count) break;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[4 * j] += f[h][j].x;
+          v[4 * j + 1] += f[h][j].y;
+          v[4 * j + 2] += f[h][j].z;
+          v[4 * j + 3] += f[h][j].w;
+        }
       }
     }
     tmem_st32(ta + col, v);
@@ -812,10 +821,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kMaxDevices = 64;
 constexpr int kMaxPairs = 80;           // pairs of a launch at most (slots of the workspace)
 #ifndef DT_JOIN
-#define DT_JOIN 10
+#define DT_JOIN 14
 #endif
 #ifndef DT_MIN
-#define DT_MIN 4
+#define DT_MIN 8
 #endif
 constexpr int kJoinSteps = DT_JOIN, kMinSteps = DT_MIN;
 
@@ -861,9 +870,13 @@ cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   pairs = std::min(pairs, kMaxPairs);
   // The tail: the tiles behind the last full wave, when spreading them over
-  // all pairs saves more than joining their pieces costs.  A plain last wave
-  // takes a tile's steps; spread, the share of it that the tail fills, plus
-  // about kJoinSteps for the partial tiles' way through L2.
+  // more pairs saves more than joining their pieces costs.  A plain last wave
+  // takes a tile's steps; spread over W workers, total / W steps and the join:
+  // the partial tiles' way through L2 and back, about kJoinSteps plus two a
+  // piece (bf16, 256 x 14336 x 4096: 81 us plain, 51 us in pieces; 512 x 4096 x
+  // 14336: 54.5 us plain, 61 us in pieces).  W is a multiple of the tail's
+  // tiles where that leaves each tile at least two pieces (a share that
+  // straddles two tiles adds a piece to both).
   const int tiles = P.pr[P.nprob - 1].tile_end, last = tiles % pairs;
   P.dp_tiles = tiles;
   P.workers = 0;
@@ -882,8 +895,10 @@ cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
     P.tail_step[P.nprob] = total;
     // at least kMinSteps a worker, at most kMaxPieces pieces a tile
     const int64_t least = std::max<int64_t>(kMinSteps, (deepest + kMaxPieces - 3) / (kMaxPieces - 2));
-    const int workers = (int)std::min<int64_t>(pairs, total / least);
-    if (workers > last && (double)total / workers + kJoinSteps < deepest) {
+    int workers = (int)std::min<int64_t>(pairs, total / least);
+    if (workers >= 2 * last) workers -= workers % last;
+    if (workers > last &&
+        (double)total / workers + kJoinSteps + 2.0 * ((workers + last - 1) / last) < (double)deepest) {
       P.dp_tiles = dp;
       P.workers = workers;
     }
