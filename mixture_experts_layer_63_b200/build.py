@@ -20,8 +20,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["moe_api.cu", "router_gate.cu", "permute.cu", "gemm_sm100.cu", "ffn_f32.cu",
-           "combine.cu", "backward.cu", "router_tc.cu", "dense_api.cu", "dense_simt.cu", "dense_tc.cu", "dense_few.cu", "dense_pack.cu",
-           "clip.cu"]
+           "combine.cu", "backward.cu", "router_tc.cu", "dense_api.cu", "dense_simt.cu",
+           "dense_tc.cu", "dense_few.cu", "dense_rows.cu", "dense_pack.cu", "clip.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

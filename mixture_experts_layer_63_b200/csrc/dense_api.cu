@@ -140,6 +140,8 @@ class Products {
   cudaError_t run(DenseGemm *g, int n) {
     uint32_t *err = reinterpret_cast<uint32_t *>(base_);
     if (n == 1 && dense_few_ok(g[0])) return launch_dense_few(g[0], err, s_);
+    if (n == 1 && dense_rows_ok(g[0]) && (dtype_ == MOE_F32 || !dense_tc_ok(g[0])))
+      return launch_dense_rows(g[0], s_);
     double macs = 0;
     for (int i = 0; i < n; ++i) macs += (double)g[i].M * g[i].N * g[i].K * (g[i].a2.p || g[i].b3.p ? 2 : 1);
     if (macs >= kTcMacs || dtype_ == MOE_BF16) {

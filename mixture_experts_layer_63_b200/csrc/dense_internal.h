@@ -80,6 +80,11 @@ cudaError_t launch_pack(int dtype, const PackJob *jobs, int n, cudaStream_t s);
 bool dense_few_ok(const DenseGemm &g);
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s);
 
+// The same on CUDA cores, any strides (dense_rows.cu): fp32, and bf16 operands
+// that are not aligned
+bool dense_rows_ok(const DenseGemm &g);
+cudaError_t launch_dense_rows(const DenseGemm &g, cudaStream_t s);
+
 // Column sums out[n] = sum_m src[m, n] (fp32, in a fixed order), up to three
 // matrices of M rows in one launch.  With z (packed [M, N])
 // and dz (lines ld_dz apart): dz = src * act'(z) first, and the sums are dz's;
