@@ -633,6 +633,12 @@ class _Args:
             return None
         return self.rows(t.view(1, -1) if t.dim() == 1 else t, 1, n, 0)
 
+    def number(self, t: torch.Tensor | None):
+        """Device pointer of a tensor of one element."""
+        if t is None or (t.get_device() == self.dev and t.dtype is self.dtype and t.numel() == 1):
+            return None if t is None else t.data_ptr()
+        return self.rows(t.reshape(1, -1), 1, 1, 0)
+
     def stream(self, stream: torch.cuda.Stream | None) -> int:
         if stream is not None:
             return stream.cuda_stream
@@ -764,7 +770,7 @@ def moe_grad_norm(grads, norm, ws, stream=None):
     arr, n = _grad_list(grads)
     q = _Args(MOE_F32)
     wp, wn = q.workspace(ws)
-    _check("moe_grad_norm", lib().moe_grad_norm(arr, n, _ptr(norm, 1, torch.float32), wp, wn, q.stream(stream)))
+    _check("moe_grad_norm", lib().moe_grad_norm(arr, n, q.number(norm), wp, wn, q.stream(stream)))
 
 
 def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
@@ -774,7 +780,7 @@ def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
     arr, n = _grad_list(grads, out)
     q = _Args(MOE_F32)
     wp, wn = q.workspace(ws)
-    _check("moe_clip_grads", lib().moe_clip_grads(arr, n, max_norm, _ptr(norm, 1, torch.float32), wp, wn,
+    _check("moe_clip_grads", lib().moe_clip_grads(arr, n, max_norm, q.number(norm), wp, wn,
                                                   q.stream(stream)))
 
 

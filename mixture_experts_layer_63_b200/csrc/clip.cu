@@ -43,16 +43,26 @@ __device__ __forceinline__ int tensor_of(const ClipTable &t, int chunk) {
   return lo;
 }
 
-// 16 bytes at a time where p is 16-byte aligned (chunks start at multiples of
-// 8 elements), element by element otherwise and behind the last full piece
+// f(i, piece i) for the 16-byte pieces of p where it is 16-byte aligned (four
+// loads in flight a thread; chunks start at multiples of 8 elements), and
+// f(i, element i) for what is left, or for everything
 template <typename T, typename F>
 __device__ __forceinline__ void each(const T *p, int64_t n, bool vec, F f) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 16 / sizeof(T), R = 4;
   int64_t done = 0;
   if (vec) {
-    const int64_t nv = n / V;
-    for (int64_t i = threadIdx.x; i < nv; i += kClipThreads) f(i, reinterpret_cast<const uint4 *>(p)[i]);
-    done = nv * V;
+    const int nv = (int)(n / V);
+    const uint4 *q = reinterpret_cast<const uint4 *>(p);
+    int i = threadIdx.x;
+    for (; i + (R - 1) * kClipThreads < nv; i += R * kClipThreads) {
+      uint4 w[R];
+#pragma unroll
+      for (int k = 0; k < R; ++k) w[k] = q[i + k * kClipThreads];
+#pragma unroll
+      for (int k = 0; k < R; ++k) f(i + k * kClipThreads, w[k]);
+    }
+    for (; i < nv; i += kClipThreads) f(i, q[i]);
+    done = (int64_t)nv * V;
   }
   for (int64_t i = done + threadIdx.x; i < n; i += kClipThreads) f(i, p[i]);
 }
@@ -141,7 +151,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   if (max_norm < 0.0f) return;
   const double ratio = (double)max_norm / (n + kClipEps);
   const float c = ratio > 1.0 ? 1.0f : (float)ratio;        // a NaN norm gives a NaN factor
-  for (int k = blockIdx.x; k < t.first[t.count]; k += gridDim.x) {
+  // last chunks first: the norm's pass read them last, so they may still be in L2
+  for (int k = t.first[t.count] - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
     const int i = tensor_of(t, k);
     if (c == 1.0f && t.dst[i] == t.src[i]) continue;
     const int64_t at = (int64_t)(k - t.first[i]) * t.chunk, m = min((int64_t)t.chunk, t.n[i] - at);

@@ -1,13 +1,16 @@
 // The dense operators' products on CUDA cores, for any strides and sizes,
-// and their elementwise and column-sum passes.
+// and their column-sum passes.
 //
 //   acc[m, n] = sum_k A(m, k) B(n, k)
 //
-// One block of 256 threads computes a 64 x 64 tile of acc (4 x 4 outputs a
-// thread) from 64 x 16 slices of A and B staged in shared memory as fp32.
-// Sums run over 512 values of k at a time and the pieces are added to a
-// second accumulator, so that a sum of K terms carries the rounding of
-// 512 + K / 512 additions instead of K.
+// One block of 256 threads computes a TS x TS tile of acc (TS / 16 squared
+// outputs a thread) from TS x 32 slices of A and B staged in shared memory as
+// fp32; the next slice is read into registers while this one is used.  Tiles
+// of 32 where 64 would leave SMs without one: what runs here is small (fp32
+// products below the tensor cores' break-even: 256 x 64 x 128 takes 6 us),
+// or cannot be read by TMA.  Sums run over 512 values of k at a time and the
+// pieces are added to a second accumulator, so that a sum of K terms carries
+// the rounding of 512 + K / 512 additions instead of K.
 #include <algorithm>
 
 #include "dense_internal.h"
@@ -16,26 +19,39 @@
 namespace moe {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 16;
-constexpr int kChunk = 512 / TK;        // slices summed before they join the second accumulator
+constexpr int TK = 32;
+constexpr int kChunk = 512;            // values of k summed before they join the second accumulator
 
-// rows r0..r0+63, columns k0..k0+15 of an operand into dst[k][row]; zero
-// outside [0, rows) x [0, K).  The 256 threads run along the contiguous
-// index (K-major: 16 k by 16 rows; else 64 rows by 4 k).
-template <typename T>
-__device__ __forceinline__ void load_slice(const Operand &o, int64_t r0, int64_t rows, int64_t k0,
-                                           int64_t K, float (*dst)[TM + 1]) {
-  const T *p = static_cast<const T *>(o.p);
-  const bool kmajor = o.ks == 1;
-#pragma unroll
-  for (int i = 0; i < TM * TK / 256; ++i) {
+// A thread's share of rows r0 ... r0 + TS - 1, columns k0 ... k0 + 31 of an
+// operand; zero outside [0, rows) x [0, K).  The threads run along the
+// contiguous index (K-major: 32 k by 8 rows; else TS rows by 256 / TS k).
+template <typename T, int TS>
+struct Slice {
+  static constexpr int N = TS * TK / 256;
+  float v[N];
+  __device__ __forceinline__ static void at(const Operand &o, int i, int &r, int &k) {
     const int e = threadIdx.x + 256 * i;
-    const int k = kmajor ? e % TK : e / TM, r = kmajor ? e / TK : e % TM;
-    float v = 0.0f;
-    if (r0 + r < rows && k0 + k < K) v = to_f32(p[(r0 + r) * o.rs + (k0 + k) * o.ks]);
-    dst[k][r] = v;
+    k = o.ks == 1 ? e % TK : e / TS;
+    r = o.ks == 1 ? e / TK : e % TS;
   }
-}
+  __device__ __forceinline__ void fetch(const Operand &o, int64_t r0, int64_t rows, int64_t k0, int64_t K) {
+    const T *p = static_cast<const T *>(o.p);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int r, k;
+      at(o, i, r, k);
+      v[i] = r0 + r < rows && k0 + k < K ? to_f32(p[(r0 + r) * o.rs + (k0 + k) * o.ks]) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void put(const Operand &o, float (*dst)[TS + 1]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      int r, k;
+      at(o, i, r, k);
+      dst[k][r] = v[i];
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, float acc, float acc3) {
@@ -76,57 +92,70 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
   }
 }
 
-template <typename T, bool GATED>
-__global__ void __launch_bounds__(256) dense_simt_kernel(const DenseGemm P) {
-  __shared__ float As[TK][TM + 1], Bs[TK][TN + 1], Cs[GATED ? TK : 1][TN + 1];
-  const int64_t mt = (P.M + TM - 1) / TM;
-  const int64_t tiles = mt * ((P.N + TN - 1) / TN);
+template <typename T, bool GATED, int TS>
+__global__ void __launch_bounds__(256) dense_simt_kernel(const __grid_constant__ DenseGemm P) {
+  constexpr int R = TS / 16;
+  __shared__ float As[TK][TS + 1], Bs[TK][TS + 1], Cs[GATED ? TK : 1][TS + 1];
+  const int64_t mt = (P.M + TS - 1) / TS;
+  const int64_t tiles = mt * ((P.N + TS - 1) / TS);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   pdl_wait();
   pdl_trigger();
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t m0 = tile % mt * TM, n0 = tile / mt * TN;
-    float acc[4][4] = {}, acc3[4][4] = {};
+    const int64_t m0 = tile % mt * TS, n0 = tile / mt * TS;
+    float acc[R][R] = {}, acc3[R][R] = {};
     for (int seg = 0; seg < (P.a2.p ? 2 : 1); ++seg) {
       const Operand a = seg ? P.a2 : P.a, b = seg ? P.b2 : P.b;
-      for (int64_t k0 = 0; k0 < P.K; k0 += TK * kChunk) {
-        float part[4][4] = {}, part3[4][4] = {};
-        for (int64_t k = k0; k < P.K && k < k0 + TK * kChunk; k += TK) {
-          __syncthreads();
-          load_slice<T>(a, m0, P.M, k, P.K, As);
-          load_slice<T>(b, n0, P.N, k, P.K, Bs);
-          if (GATED) load_slice<T>(P.b3, n0, P.N, k, P.K, Cs);
-          __syncthreads();
+      Slice<T, TS> sa, sb, sc;
+      float part[R][R] = {}, part3[R][R] = {};
+      auto fetch = [&](int64_t k) {
+        sa.fetch(a, m0, P.M, k, P.K);
+        sb.fetch(b, n0, P.N, k, P.K);
+        if (GATED) sc.fetch(P.b3, n0, P.N, k, P.K);
+      };
+      if (P.K > 0) fetch(0);
+      for (int64_t k = 0; k < P.K; k += TK) {
+        __syncthreads();
+        sa.put(a, As);
+        sb.put(b, Bs);
+        if (GATED) sc.put(P.b3, Cs);
+        __syncthreads();
+        if (k + TK < P.K) fetch(k + TK);
 #pragma unroll
-          for (int kk = 0; kk < TK; ++kk) {
-            float av[4];
+        for (int kk = 0; kk < TK; ++kk) {
+          float av[R];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) av[i] = As[kk][ty + 16 * i];
+          for (int i = 0; i < R; ++i) av[i] = As[kk][ty + 16 * i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float bv = Bs[kk][tx + 16 * j];
-              const float cv = GATED ? Cs[kk][tx + 16 * j] : 0.0f;
+          for (int j = 0; j < R; ++j) {
+            const float bv = Bs[kk][tx + 16 * j];
+            const float cv = GATED ? Cs[kk][tx + 16 * j] : 0.0f;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                part[i][j] = fmaf(av[i], bv, part[i][j]);
-                if (GATED) part3[i][j] = fmaf(av[i], cv, part3[i][j]);
-              }
+            for (int i = 0; i < R; ++i) {
+              part[i][j] = fmaf(av[i], bv, part[i][j]);
+              if (GATED) part3[i][j] = fmaf(av[i], cv, part3[i][j]);
             }
           }
         }
+        if ((k + TK) % kChunk == 0 || k + TK >= P.K) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j] += part[i][j];
-            if (GATED) acc3[i][j] += part3[i][j];
-          }
+            for (int j = 0; j < R; ++j) {
+              acc[i][j] += part[i][j];
+              part[i][j] = 0.0f;
+              if (GATED) {
+                acc3[i][j] += part3[i][j];
+                part3[i][j] = 0.0f;
+              }
+            }
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < R; ++j) {
         const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
         if (m < P.M && n < P.N) store1<T>(P, m, (int)n, acc[i][j], acc3[i][j]);
       }
@@ -273,22 +302,22 @@ cudaError_t colsums_as(const ColSums &P, int count, int maxN, int act, bool join
   return launch_kernel(colsum_join_kernel<T>, dim3((maxN + 31) / 32, 1, count), 256, 0, s, P);
 }
 
-unsigned grid_for(int64_t blocks, int per_sm) {
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)device_sms() * per_sm));
+template <typename T, bool GATED>
+cudaError_t simt_as(const DenseGemm &g, cudaStream_t s) {
+  auto tiles = [&](int ts) { return ((g.M + ts - 1) / ts) * (((int64_t)g.N + ts - 1) / ts); };
+  if (tiles(64) == 0) return cudaSuccess;
+  const int64_t most = (int64_t)device_sms() * 8;
+  return tiles(64) >= device_sms()
+             ? launch_kernel(dense_simt_kernel<T, GATED, 64>, (unsigned)std::min(tiles(64), most), 256, 0, s, g)
+             : launch_kernel(dense_simt_kernel<T, GATED, 32>, (unsigned)std::min(tiles(32), most), 256, 0, s, g);
 }
 
 }  // namespace
 
 cudaError_t launch_dense_simt(const DenseGemm &g, cudaStream_t s) {
-  const int64_t tiles = ((g.M + TM - 1) / TM) * ((g.N + TN - 1) / TN);
-  if (tiles == 0) return cudaSuccess;
-  const unsigned grid = grid_for(tiles, 8);
   const bool gated = g.epi == kDenseGated;
-  if (g.dtype == MOE_F32)
-    return gated ? launch_kernel(dense_simt_kernel<float, true>, grid, 256, 0, s, g)
-                 : launch_kernel(dense_simt_kernel<float, false>, grid, 256, 0, s, g);
-  return gated ? launch_kernel(dense_simt_kernel<__nv_bfloat16, true>, grid, 256, 0, s, g)
-               : launch_kernel(dense_simt_kernel<__nv_bfloat16, false>, grid, 256, 0, s, g);
+  if (g.dtype == MOE_F32) return gated ? simt_as<float, true>(g, s) : simt_as<float, false>(g, s);
+  return gated ? simt_as<__nv_bfloat16, true>(g, s) : simt_as<__nv_bfloat16, false>(g, s);
 }
 
 size_t colsum_scratch(int64_t M, int N, int count) { return (size_t)colsum_parts(M, N) * N * 4 * count; }
