@@ -33,21 +33,15 @@ namespace {
 
 constexpr int BM = 128;                 // rows of a CTA's half tile
 constexpr int BK = 64;
-#ifndef DT_BKS
-#define DT_BKS 2
-#endif
-#ifndef DT_GM
-#define DT_GM 16
-#endif
-constexpr int kBks = DT_BKS;                 // k-blocks of a stage
+constexpr int kBks = 2;                      // k-blocks of a stage
 constexpr int kStages = 6 / kBks;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kRegsLaunch = 168, kRegsLow = 56, kRegsHigh = 224;
+constexpr int kRegsLaunch = 168, kRegsLow = 88, kRegsHigh = 208;
 constexpr int kAccCols = 256;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kABytes = BM * BK * 2;
-constexpr int kGroupM = DT_GM;                   // row tiles of a raster group
+constexpr int kGroupM = 16;                  // row tiles of a raster group
 constexpr int kMaxProblems = 4;
 constexpr int kMaxSegs = 12;
 
@@ -218,35 +212,43 @@ struct Rows {
   __device__ Rows(const void *q, int64_t ld_, int64_t M_, int N_)
       : p(static_cast<T *>(const_cast<void *>(q))), ld(ld_), M(M_), N(N_),
         vec(((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(ld_ * (int64_t)sizeof(T))) & 15) == 0) {}
-  // the warp's chunk lies inside and moves in whole pieces: one branch a
-  // chunk (a branch a piece serialises the accesses)
-  __device__ __forceinline__ bool whole(int64_t row0, int col) const {
-    return vec && row0 + 32 <= M && col + kCols<T> <= N;
-  }
-  __device__ __forceinline__ uint4 load(int64_t row, int col) const {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (row >= M || col >= N) return w;
-    const T *q = p + row * ld + col;
-    if (vec && col + E <= N) return *reinterpret_cast<const uint4 *>(q);
-    float v[E];
-#pragma unroll
-    for (int k = 0; k < E; ++k) v[k] = col + k < N ? to_f32(q[k]) : 0.0f;
-    return pack16<T>(v);
-  }
-  __device__ __forceinline__ void store(int64_t row, int col, const uint4 &w) const {
-    if (row >= M || col >= N) return;
-    T *q = p + row * ld + col;
-    if (vec && col + E <= N) {
-      *reinterpret_cast<uint4 *>(q) = w;
-      return;
-    }
-    float v[E];
-    unpack16<T>(w, v);
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (col + k < N) from_f32(q[k], v[k]);
-  }
+  // the chunk moves in whole pieces (of the rows and pieces that exist): one
+  // branch a chunk, predicates within it (a branch a piece serialises the
+  // accesses: the gradient epilogue alone took 211 us with it, 160 without)
+  __device__ __forceinline__ bool pieces(int col) const { return vec && (col + kCols<T> <= N || N % E == 0); }
 };
+
+// Element by element, for rows that are not 16-byte aligned and the matrix's
+// edges: instruction i of a warp covers 32 consecutive elements of the chunk,
+// so that its lanes touch whole row stretches.  Calls of their own, so that
+// the common path keeps its registers and its instruction cache lines.
+template <typename T>
+__device__ __forceinline__ T &staged(uint4 *stg, int r, int c) {
+  constexpr int E = 16 / sizeof(T);
+  return reinterpret_cast<T *>(stg + stg_at(r, c / E))[c % E];
+}
+// p: row row0, column col; rows, cols: what lies inside the matrix
+template <typename T>
+__device__ __noinline__ void store_edge(T *p, int64_t ld, int rows, int cols, uint4 *stg, int lane) {
+  constexpr int CW = kCols<T>;
+#pragma unroll 8
+  for (int i = 0; i < CW; ++i) {
+    const int r = i * (32 / CW) + lane / CW, c = lane % CW;
+    if (r < rows && c < cols) p[r * ld + c] = staged<T>(stg, r, c);
+  }
+}
+template <typename T>
+__device__ __noinline__ void load_edge(const T *p, int64_t ld, int rows, int cols, uint4 *stg, int lane) {
+  constexpr int CW = kCols<T>;
+#pragma unroll 8
+  for (int i = 0; i < CW; ++i) {
+    const int r = i * (32 / CW) + lane / CW, c = lane % CW;
+    T v;
+    from_f32(v, 0.0f);
+    if (r < rows && c < cols) v = p[r * ld + c];
+    staged<T>(stg, r, c) = v;
+  }
+}
 
 // each thread's row, four packed pieces, to rows row0 ... of `o`
 template <typename T>
@@ -256,15 +258,17 @@ __device__ __forceinline__ void store_chunk(const Rows<T> &o, int64_t row0, int 
   for (int c = 0; c < 4; ++c) stg[stg_at(lane, c)] = w[c];
   __syncwarp();
   const int r0 = lane / 4, c = lane % 4;
-  if (o.whole(row0, col)) {
+  if (o.pieces(col)) {
     uint4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = stg[stg_at(i * 8 + r0, c)];
     T *q = o.p + (row0 + r0) * o.ld + col + c * o.E;
+    const int rows = col + c * o.E < o.N ? (int)min((int64_t)32, o.M - row0) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(q + i * 8 * o.ld) = v[i];
+    for (int i = 0; i < 4; ++i)
+      if (i * 8 + r0 < rows) *reinterpret_cast<uint4 *>(q + i * 8 * o.ld) = v[i];
   } else {
-    for (int i = 0; i < 4; ++i) o.store(row0 + i * 8 + r0, col + c * o.E, stg[stg_at(i * 8 + r0, c)]);
+    store_edge<T>(o.p + row0 * o.ld + col, o.ld, (int)min((int64_t)32, o.M - row0), o.N - col, stg, lane);
   }
   __syncwarp();
 }
@@ -279,23 +283,28 @@ __device__ __forceinline__ void store_vals(const Rows<T> &o, int64_t row0, int c
 }
 
 // a chunk on its way in: whole row pieces in registers, then staged so that
-// each thread finds its row (after a __syncwarp)
+// each thread finds its row (after a __syncwarp); a chunk that does not move
+// in whole pieces is read when it is staged (zeros beyond the matrix)
 template <typename T>
 struct Incoming {
   uint4 w[4];
   __device__ __forceinline__ void fetch(const Rows<T> &o, int64_t row0, int col, int lane) {
-    if (o.whole(row0, col)) {
-      const T *q = o.p + (row0 + lane / 4) * o.ld + col + lane % 4 * o.E;
+    if (!o.pieces(col)) return;
+    const T *q = o.p + (row0 + lane / 4) * o.ld + col + lane % 4 * o.E;
+    const int rows = col + lane % 4 * o.E < o.N ? (int)min((int64_t)32, o.M - row0) : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(q + i * 8 * o.ld);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = o.load(row0 + i * 8 + lane / 4, col + lane % 4 * o.E);
+    for (int i = 0; i < 4; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (i * 8 + lane / 4 < rows) w[i] = *reinterpret_cast<const uint4 *>(q + i * 8 * o.ld);
     }
   }
-  __device__ __forceinline__ void stage(uint4 *stg, int lane) const {
+  __device__ __forceinline__ void stage(const Rows<T> &o, int64_t row0, int col, uint4 *stg, int lane) const {
+    if (o.pieces(col)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) stg[stg_at(i * 8 + lane / 4, lane % 4)] = w[i];
+      for (int i = 0; i < 4; ++i) stg[stg_at(i * 8 + lane / 4, lane % 4)] = w[i];
+    } else {
+      load_edge<T>(o.p + row0 * o.ld + col, o.ld, (int)min((int64_t)32, o.M - row0), o.N - col, stg, lane);
+    }
   }
 };
 
@@ -375,7 +384,7 @@ struct Epilogue {
           for (int i = 0; i < CW; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]);
         });
         if (Q.residual) {
-          in[0].stage(stg, lane);
+          in[0].stage(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col, stg, lane);
           __syncwarp();
           fetch(c + CW);
 #pragma unroll
@@ -409,8 +418,8 @@ struct Epilogue {
         // a and u staged side by side; dA, dU and h packed piece by piece, so
         // that no more than one matrix is held in fp32
         uint4 *stg_u = stg + (kIn - 1) * (kStgBytes / 16);
-        in[0].stage(stg, lane);
-        in[kIn - 1].stage(stg_u, lane);
+        in[0].stage(packed(Q.pre_in), row0, col, stg, lane);
+        in[kIn - 1].stage(packed(Q.pre3_in), row0, col, stg_u, lane);
         __syncwarp();
         fetch(c + CW);
         acc_cols(taddr + c, v);
@@ -464,9 +473,9 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 // Accumulator column of a warp's group i of 32 (its half of the output
 // columns; gated: of the gate's, then of the up-projection's); -1: none
 template <int EPI>
-__device__ __forceinline__ int group_col(const TcParams &P, int half, int i) {
-  const int w = P.bnh / 2, g = EPI == kDenseGated ? i >> 1 : 0, c = 32 * (EPI == kDenseGated ? i & 1 : i);
-  return c < w ? g * P.bnh + half * w + c : -1;
+__device__ __forceinline__ int group_col(int bnh, int half, int i) {
+  const int w = bnh / 2, g = EPI == kDenseGated ? i >> 1 : 0, c = 32 * (EPI == kDenseGated ? i & 1 : i);
+  return c < w ? g * bnh + half * w + c : -1;
 }
 
 // A piece that is not the whole tile: this warp's part of the accumulator to
@@ -481,14 +490,16 @@ constexpr int64_t kSlotFloats = 2 * BM * kAccCols;    // a pair's accumulators
 static_assert(kTailCountOffset + 4 * 2 * kMaxTail <= kCtrlBytes, "counters of the tail");
 
 template <int EPI>
-__device__ bool join_pieces(const TcParams &P, const Piece &pc, uint32_t ta, int rank, int ew, int half, int lane) {
-  auto at = [&](int slot) {
-    return reinterpret_cast<float4 *>(P.part + slot * kSlotFloats) + (rank * kEpiWarps + ew) * (4 * 8 * 32) + lane;
+__device__ __noinline__ bool join_pieces(float *parts, uint32_t *count, int bnh, int slot, int first_worker, int pieces,
+                                         uint32_t ta, int rank, int ew, int lane) {
+  const int half = ew >> 2;
+  auto at = [&](int64_t slot) {
+    return reinterpret_cast<float4 *>(parts + slot * kSlotFloats) + (rank * kEpiWarps + ew) * (4 * 8 * 32) + lane;
   };
-  float4 *mine = at(pc.slot);
+  float4 *mine = at(slot);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int col = group_col<EPI>(P, half, i);
+    const int col = group_col<EPI>(bnh, half, i);
     if (col < 0) continue;
     uint32_t r[32];
     tmem_ld32(ta + col, r);
@@ -500,35 +511,34 @@ __device__ bool join_pieces(const TcParams &P, const Piece &pc, uint32_t ta, int
   }
   __threadfence();
   __syncwarp();
-  uint32_t *count = P.err + kTailCountOffset / 4 + pc.tail * 2 + rank;
   int last = 0;
   if (lane == 0) {
     const uint32_t old = atomicAdd(count, 1u << (4 * ew));
-    last = (int)((old >> (4 * ew)) & 15u) == pc.count - 1;
-    if (last) atomicSub(count, (uint32_t)pc.count << (4 * ew));
+    last = (int)((old >> (4 * ew)) & 15u) == pieces - 1;
+    if (last) atomicSub(count, (uint32_t)pieces << (4 * ew));
   }
   last = __shfl_sync(0xffffffffu, last, 0);
   if (!last) return false;
   __threadfence();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int col = group_col<EPI>(P, half, i);
+    const int col = group_col<EPI>(bnh, half, i);
     if (col < 0) continue;
     // two pieces in flight
     float v[32] = {};
-    for (int k = 0; k < pc.count; k += 2) {
+    for (int k = 0; k < pieces; k += 2) {
       float4 f[2][8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (k + h >= pc.count) break;
+        if (k + h >= pieces) break;
         // piece 0 is the end of its worker's share, the others begin theirs
-        const float4 *src = at(2 * (pc.first_worker + k + h) + (k + h == 0 ? 1 : 0)) + i * 8 * 32;
+        const float4 *src = at(2 * (first_worker + k + h) + (k + h == 0 ? 1 : 0)) + i * 8 * 32;
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[h][j] = __ldcg(src + j * 32);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (k + h >= pc.count) break;
+        if (k + h >= pieces) break;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[4 * j] += f[h][j].x;
@@ -599,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // Registers: 168 a thread at launch (384 threads); the four warps of the
   // first warpgroup give most of theirs to the epilogue:
-  // 128 * 56 + 256 * 224 = 384 * 168
+  // 128 * 88 + 256 * 208 = 384 * 168
   static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * kRegsLaunch, "registers of the block");
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
@@ -773,7 +783,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int col = group_col<EPI>(P, half, i);
+            const int col = group_col<EPI>(P.bnh, half, i);
             if (col < 0) continue;
             uint32_t r[32];
             tmem_ld32(ta + col, r);
@@ -799,7 +809,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
       bool finish = true;
       if (!pc.whole()) {
-        finish = join_pieces<EPI>(P, pc, ta, (int)rank, ew, half, lane);
+        finish = join_pieces<EPI>(P.part, P.err + kTailCountOffset / 4 + pc.tail * 2 + rank, P.bnh, pc.slot,
+                                  pc.first_worker, pc.count, ta, (int)rank, ew, lane);
         if (finish) ep.begin();
       }
       if (finish) ep.run(ta, sb);
@@ -820,13 +831,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // ------------------------------- host side --------------------------------------
 constexpr int kMaxDevices = 64;
 constexpr int kMaxPairs = 80;           // pairs of a launch at most (slots of the workspace)
-#ifndef DT_JOIN
-#define DT_JOIN 14
-#endif
-#ifndef DT_MIN
-#define DT_MIN 8
-#endif
-constexpr int kJoinSteps = DT_JOIN, kMinSteps = DT_MIN;
+constexpr int kJoinSteps = 14, kMinSteps = 8;
 
 // As many CTA pairs as fit at once.  The attribute is set and the occupancy
 // asked once a device (a second thread that asks meanwhile gets the same).
@@ -963,8 +968,8 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
   P.part = part;
   P.act = g[0].act;
   P.nprob = n;
-  // columns of a tile: 128 where that saves more than its dearer product (a
-  // 128-column tile costs about 0.55 of a 256-column one)
+  // columns of a tile: 256, or 128 (about 0.8 of the time each) where that
+  // spreads a small product over more pairs or pads less
   const bool gated = g[0].epi == kDenseGated;
   auto tiles_of = [&](const DenseGemm &q, int bn) {
     const int w = gated ? bn / 2 : bn;
@@ -975,7 +980,9 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
     for (int p = 0; p < n; ++p) t += tiles_of(g[p], bn);
     return t;
   };
-  P.bn = 0.55 * (double)tiles_at(128) < (double)tiles_at(256) ? 128 : 256;
+  const double pairs = std::max(1, device_sms() / 2);
+  auto cost = [&](int bn) { return std::max(1.0, (double)tiles_at(bn) / pairs) * (bn == 256 ? 1.0 : 0.8); };
+  P.bn = cost(128) < cost(256) ? 128 : 256;
   P.bnh = gated ? P.bn / 2 : P.bn;
   if (tiles_at(P.bn) > 0x3fffffff) return cudaErrorInvalidValue;
   auto box_b = [&](const Operand &o) { return kmajor(o) ? P.bn / 2 : BK; };
