@@ -282,6 +282,16 @@ __device__ __forceinline__ void store_vals(const Rows<T> &o, int64_t row0, int c
   store_chunk(o, row0, col, w, stg, lane);
 }
 
+// 16 bytes; the 256-byte stretch around them is brought to L2, where the
+// chunks to come find it
+__device__ __forceinline__ uint4 ld16_ahead(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // a chunk on its way in: whole row pieces in registers, then staged so that
 // each thread finds its row (after a __syncwarp); a chunk that does not move
 // in whole pieces is read when it is staged (zeros beyond the matrix)
@@ -295,7 +305,7 @@ struct Incoming {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       w[i] = make_uint4(0, 0, 0, 0);
-      if (i * 8 + lane / 4 < rows) w[i] = *reinterpret_cast<const uint4 *>(q + i * 8 * o.ld);
+      if (i * 8 + lane / 4 < rows) w[i] = ld16_ahead(q + i * 8 * o.ld);
     }
   }
   __device__ __forceinline__ void stage(const Rows<T> &o, int64_t row0, int col, uint4 *stg, int lane) const {
