@@ -240,14 +240,15 @@ __device__ __noinline__ void store_edge(T *p, int64_t ld, int rows, int cols, ui
 template <typename T>
 __device__ __noinline__ void load_edge(const T *p, int64_t ld, int rows, int cols, uint4 *stg, int lane) {
   constexpr int CW = kCols<T>;
-#pragma unroll 8
+  T v[CW];                       // all of them in flight
+#pragma unroll
   for (int i = 0; i < CW; ++i) {
     const int r = i * (32 / CW) + lane / CW, c = lane % CW;
-    T v;
-    from_f32(v, 0.0f);
-    if (r < rows && c < cols) v = p[r * ld + c];
-    staged<T>(stg, r, c) = v;
+    from_f32(v[i], 0.0f);
+    if (r < rows && c < cols) v[i] = p[r * ld + c];
   }
+#pragma unroll
+  for (int i = 0; i < CW; ++i) staged<T>(stg, i * (32 / CW) + lane / CW, lane % CW) = v[i];
 }
 
 // each thread's row, four packed pieces, to rows row0 ... of `o`
