@@ -143,8 +143,12 @@ class Products {
     if (n == 1 && dense_rows_ok(g[0]) && (dtype_ == MOE_F32 || !dense_tc_ok(g[0])))
       return launch_dense_rows(g[0], s_);
     double macs = 0;
-    for (int i = 0; i < n; ++i) macs += (double)g[i].M * g[i].N * g[i].K * (g[i].a2.p || g[i].b3.p ? 2 : 1);
-    if (macs >= kTcMacs || dtype_ == MOE_BF16) {
+    int64_t depth = 0;
+    for (int i = 0; i < n; ++i) {
+      macs += (double)g[i].M * g[i].N * g[i].K * (g[i].a2.p || g[i].b3.p ? 2 : 1);
+      depth = std::max(depth, g[i].K);
+    }
+    if (macs >= kTcMacs || depth > kSimtDepth || dtype_ == MOE_BF16) {
       DenseGemm q[4];
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
@@ -173,6 +177,9 @@ class Products {
   // fewer multiply-adds than this stay on the CUDA cores in fp32: the splits
   // and the tensor-core launch cost more than they save
   static constexpr double kTcMacs = 1 << 22;
+  // ... unless a contraction is longer than this, which one CUDA-core block
+  // would run through alone
+  static constexpr int64_t kSimtDepth = 512;
   static constexpr int kMaxJobs = 8;
 
   // `o`, rows x K, replaced by its copy where the tensor cores need one

@@ -483,10 +483,11 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // Accumulator column of a warp's group i of 32 (its half of the output
 // columns; gated: of the gate's, then of the up-projection's); -1: none
+// (cols: the tile's output columns that exist)
 template <int EPI>
-__device__ __forceinline__ int group_col(int bnh, int half, int i) {
+__device__ __forceinline__ int group_col(int bnh, int cols, int half, int i) {
   const int w = bnh / 2, g = EPI == kDenseGated ? i >> 1 : 0, c = 32 * (EPI == kDenseGated ? i & 1 : i);
-  return c < w ? g * bnh + half * w + c : -1;
+  return c < w && half * w + c < cols ? g * bnh + half * w + c : -1;
 }
 
 // A piece that is not the whole tile: this warp's part of the accumulator to
@@ -501,7 +502,7 @@ constexpr int64_t kSlotFloats = 2 * BM * kAccCols;    // a pair's accumulators
 static_assert(kTailCountOffset + 4 * 2 * kMaxTail <= kCtrlBytes, "counters of the tail");
 
 template <int EPI>
-__device__ __noinline__ bool join_pieces(float *parts, uint32_t *count, int bnh, int slot, int first_worker, int pieces,
+__device__ __noinline__ bool join_pieces(float *parts, uint32_t *count, int bnh, int cols, int slot, int first_worker, int pieces,
                                          uint32_t ta, int rank, int ew, int lane) {
   const int half = ew >> 2;
   auto at = [&](int64_t slot) {
@@ -510,7 +511,7 @@ __device__ __noinline__ bool join_pieces(float *parts, uint32_t *count, int bnh,
   float4 *mine = at(slot);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int col = group_col<EPI>(bnh, half, i);
+    const int col = group_col<EPI>(bnh, cols, half, i);
     if (col < 0) continue;
     uint32_t r[32];
     tmem_ld32(ta + col, r);
@@ -533,7 +534,7 @@ __device__ __noinline__ bool join_pieces(float *parts, uint32_t *count, int bnh,
   __threadfence();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int col = group_col<EPI>(bnh, half, i);
+    const int col = group_col<EPI>(bnh, cols, half, i);
     if (col < 0) continue;
     // two pieces in flight
     float v[32] = {};
@@ -794,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int col = group_col<EPI>(P.bnh, half, i);
+            const int col = group_col<EPI>(P.bnh, Q.N - col0, half, i);
             if (col < 0) continue;
             uint32_t r[32];
             tmem_ld32(ta + col, r);
@@ -820,7 +821,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
       bool finish = true;
       if (!pc.whole()) {
-        finish = join_pieces<EPI>(P.part, P.err + kTailCountOffset / 4 + pc.tail * 2 + rank, P.bnh, pc.slot,
+        // (a warp without rows has nothing to join, in any piece)
+        finish = ep.row0 < Q.M && join_pieces<EPI>(P.part, P.err + kTailCountOffset / 4 + pc.tail * 2 + rank, P.bnh, Q.N - col0, pc.slot,
                                   pc.first_worker, pc.count, ta, (int)rank, ew, lane);
         if (finish) ep.begin();
       }
@@ -913,8 +915,8 @@ cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
     const int64_t least = std::max<int64_t>(kMinSteps, (deepest + kMaxPieces - 3) / (kMaxPieces - 2));
     int workers = (int)std::min<int64_t>(pairs, total / least);
     if (workers >= 2 * last) workers -= workers % last;
-    if (workers > last &&
-        (double)total / workers + kJoinSteps + 2.0 * ((workers + last - 1) / last) < (double)deepest) {
+    if (workers > 0 &&
+        (double)total / workers + kJoinSteps + 2.0 * deepest * workers / total < (double)deepest) {
       P.dp_tiles = dp;
       P.workers = workers;
     }
@@ -997,10 +999,10 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
   P.bnh = gated ? P.bn / 2 : P.bn;
   if (tiles_at(P.bn) > 0x3fffffff) return cudaErrorInvalidValue;
   auto box_b = [&](const Operand &o) { return kmajor(o) ? P.bn / 2 : BK; };
-  // longest contractions first: the last wave is then one of short tiles
+  // longest contractions last: they are then in the tail, which can be cut
   int order[kMaxProblems] = {0, 1, 2, 3};
   auto depth = [&](int p) { return g[p].K * (g[p].a2.p ? 2 : 1); };
-  std::stable_sort(order, order + n, [&](int a, int b) { return depth(a) > depth(b); });
+  std::stable_sort(order, order + n, [&](int a, int b) { return depth(a) < depth(b); });
   int64_t end = 0;
   for (int p = 0; p < n; ++p) {
     TcProblem &Q = P.pr[p];
