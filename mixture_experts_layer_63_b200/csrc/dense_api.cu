@@ -109,6 +109,17 @@ size_t pack_room(int dtype, int64_t lines, int64_t inner, int64_t ld) {
   return align256(pack_bytes(dtype, lines, inner));
 }
 
+// bf16 calls of few rows hand dz, h, dA and dU from one product to the next in
+// two planes (the value rounded to bf16, and the rest rounded): 16 significant
+// bits instead of 8, so that their results carry one rounding.  (Of more rows
+// the errors average out in the sums.)  Forward the time is the weights'
+// stream, and the second plane is free: up to 16 rows.  Backward it doubles
+// products that are short beside their launches (one row of a 2048 / 5632
+// block: 111 us against 83): up to 4 rows.
+int planes_of(int dtype, int64_t rows, bool backward) {
+  return dtype == MOE_BF16 && rows <= (backward ? 4 : 16) ? 2 : 1;
+}
+
 struct LinearLayout {
   size_t dz, part, tail, pack, total;
 };
@@ -119,7 +130,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
   size_t room = pack_room(c.dtype, c.M, c.K, c.ld_x) + pack_room(c.dtype, c.N, c.K, c.ld_w);
   if (backward) {
     const bool act = c.act != MOE_DENSE_IDENTITY;
-    L.dz = t.take(act ? (size_t)c.M * pack_ld(c.N) * dense_elem(c.dtype) : 0);
+    L.dz = t.take(act ? (size_t)c.M * pack_ld(c.N) * dense_elem(c.dtype) * planes_of(c.dtype, c.M, true) : 0);
     L.part = t.take(colsum_scratch(c.M, c.N, 1));
     room += pack_room(c.dtype, c.M, c.N, act ? pack_ld(c.N) : c.ld_y);
   }
@@ -180,7 +191,7 @@ class Products {
   // ... unless a contraction is longer than this, which one CUDA-core block
   // would run through alone
   static constexpr int64_t kSimtDepth = 512;
-  static constexpr int kMaxJobs = 8;
+  static constexpr int kMaxJobs = kMaxPack;
 
   // `o`, rows x K, replaced by its copy where the tensor cores need one
   bool prepare(Operand *o, int64_t rows, int64_t K) {
@@ -194,7 +205,7 @@ class Products {
       ++j;
     if (j == jobs_) {
       const size_t need = align256(pack_bytes(dtype_, lines, inner));
-      if (jobs_ == kMaxJobs || jobs_ - launched_ == kMaxPack || at_ + need > end_) return false;
+      if (jobs_ == kMaxJobs || at_ + need > end_) return false;
       job_[jobs_++] = {o->p, lines, inner, ld, base_ + at_};
       at_ += need;
     }
@@ -214,6 +225,11 @@ class Products {
   PackJob job_[kMaxJobs];
   int jobs_ = 0, launched_ = 0;
 };
+
+Operand transposed(Operand o) {
+  std::swap(o.rs, o.ks);
+  return o;
+}
 
 // out [M, N] = sum over k < K of a(m, k) b(n, k)
 DenseGemm product(int dtype, int64_t M, int64_t K, int32_t N, const Operand &a, const Operand &b, void *out,
@@ -256,7 +272,7 @@ GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
   Taker t;
   // h, dA and dU have aligned lines of their own
   const int64_t T = c.T, d = c.d_model, f = c.d_ff, ldh = pack_ld(f);
-  const size_t tf = (size_t)T * ldh * dense_elem(c.dtype);
+  const size_t tf = (size_t)T * ldh * dense_elem(c.dtype) * planes_of(c.dtype, T, backward);
   auto room = [&](int64_t lines, int64_t inner, int64_t ld) { return pack_room(c.dtype, lines, inner, ld); };
   size_t pack = room(T, d, c.ld_x) + 2 * room(f, d, d) + room(d, f, f) + room(T, f, ldh);
   L.h = t.take(tf);
@@ -346,14 +362,15 @@ moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, cons
   Operand dz{dy, c.ld_y, 1};
   if (act || dbias) {
     // dz and its column sums in one pass over dy and z
-    const ColSum q{dy, c.ld_y, c.N, act ? z : nullptr, act ? base + L.dz : nullptr, pack_ld(c.N), dbias};
+    const int64_t ldz = pack_ld(c.N), lo = planes_of(c.dtype, c.M, true) == 2 ? c.M * ldz : 0;
+    const ColSum q{dy, c.ld_y, 0, c.N, act ? z : nullptr, act ? base + L.dz : nullptr, ldz, lo, dbias};
     e = launch_colsums(c.act, c.dtype, c.M, &q, 1, reinterpret_cast<float *>(base + L.part), s);
-    if (act) dz = {base + L.dz, pack_ld(c.N), 1};
+    if (act) dz = {base + L.dz, ldz, 1, lo ? 2 : 0, lo};
   }
   DenseGemm g[2] = {};
   int n = 0;
   if (dx && c.M > 0) g[n++] = product(c.dtype, c.M, c.N, c.K, dz, {w, 1, c.ld_w}, dx, c.ld_x);
-  if (dw) g[n++] = product(c.dtype, c.N, c.M, c.K, {dz.p, 1, dz.rs}, {x, 1, c.ld_x}, dw, c.K);
+  if (dw) g[n++] = product(c.dtype, c.N, c.M, c.K, transposed(dz), {x, 1, c.ld_x}, dw, c.K);
   Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
   if (e == cudaSuccess && n > 0) e = run.run(g, n);
   return dense_status(e);
@@ -402,8 +419,10 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   g.b3 = {w3, d, 1};
   g.bias = b1;
   g.bias3 = b3;
+  const int64_t lo = planes_of(c.dtype, T, false) == 2 ? T * ldh : 0;
   g.out = base + L.h;
   g.ld_o = ldh;
+  g.lo_stride = lo;
   g.pre = a;
   g.pre3 = u;
   Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
@@ -416,7 +435,7 @@ moe_status moe_gated_ffn(const moe_gated_ffn_config *cfg, const void *x, const v
   q.M = T;
   q.N = c.d_model;
   q.K = f;
-  q.a = {base + L.h, ldh, 1};
+  q.a = {base + L.h, ldh, 1, lo ? 2 : 0, lo};
   q.b = {w2, f, 1};
   q.bias = b2;
   q.residual = residual;
@@ -455,6 +474,8 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   float *part = reinterpret_cast<float *>(base + L.part);
   cudaError_t e = cudaSuccess;
   Products run(c.dtype, ws, L.tail, L.pack, L.total, s);
+  const int64_t lo = planes_of(c.dtype, T, true) == 2 ? T * ldh : 0;
+  auto hidden_rows = [&](const void *p) { return Operand{p, ldh, 1, lo ? 2 : 0, lo}; };
   if (hidden && T > 0) {
     DenseGemm g{};
     g.epi = kDenseGatedGrad;
@@ -469,6 +490,7 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
     g.pre3_in = u;
     g.out = da;
     g.ld_o = ldh;
+    g.lo_stride = lo;
     g.out2 = du;
     g.out3 = h;
     e = run.run(g);
@@ -477,21 +499,21 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
   DenseGemm g[4] = {};
   int n = 0;
   if (dx && T > 0) {
-    g[n] = product(c.dtype, T, f, c.d_model, {da, ldh, 1}, {w1, 1, d}, dx, c.ld_x);
-    g[n].a2 = {du, ldh, 1};
+    g[n] = product(c.dtype, T, f, c.d_model, hidden_rows(da), {w1, 1, d}, dx, c.ld_x);
+    g[n].a2 = hidden_rows(du);
     g[n++].b2 = {w3, 1, d};
   }
   if (dw1) {
-    g[n++] = product(c.dtype, f, T, c.d_model, {da, 1, ldh}, {x, 1, c.ld_x}, dw1, d);
-    g[n++] = product(c.dtype, f, T, c.d_model, {du, 1, ldh}, {x, 1, c.ld_x}, dw3, d);
+    g[n++] = product(c.dtype, f, T, c.d_model, transposed(hidden_rows(da)), {x, 1, c.ld_x}, dw1, d);
+    g[n++] = product(c.dtype, f, T, c.d_model, transposed(hidden_rows(du)), {x, 1, c.ld_x}, dw3, d);
   }
-  if (dw2) g[n++] = product(c.dtype, d, T, c.d_ff, {dy, 1, c.ld_y}, {h, 1, ldh}, dw2, f);
+  if (dw2) g[n++] = product(c.dtype, d, T, c.d_ff, {dy, 1, c.ld_y}, transposed(hidden_rows(h)), dw2, f);
   if (e == cudaSuccess && n > 0) e = run.run(g, n);
   ColSum bq[3];
   int nb = 0;
-  if (db1) bq[nb++] = {da, ldh, c.d_ff, nullptr, nullptr, 0, db1};
-  if (db3) bq[nb++] = {du, ldh, c.d_ff, nullptr, nullptr, 0, db3};
-  if (db2) bq[nb++] = {dy, c.ld_y, c.d_model, nullptr, nullptr, 0, db2};
+  if (db1) bq[nb++] = {da, ldh, lo, c.d_ff, nullptr, nullptr, 0, 0, db1};
+  if (db3) bq[nb++] = {du, ldh, lo, c.d_ff, nullptr, nullptr, 0, 0, db3};
+  if (db2) bq[nb++] = {dy, c.ld_y, 0, c.d_model, nullptr, nullptr, 0, 0, db2};
   if (e == cudaSuccess && nb > 0) e = launch_colsums(0, c.dtype, T, bq, nb, part, s);
   return dense_status(e);
 }

@@ -35,10 +35,11 @@ struct FewParams {
   int64_t M;
   int32_t N, KB;                 // k-blocks in all
   int32_t tt;                    // tokens of a tile (the MMA's N)
+  int32_t planes;                // of x: stacked on the MMA's N side, joined when the accumulator is read
   int32_t stages, split, tmem_cols, act;
   const void *bias, *bias3, *residual;
   void *out, *pre, *pre3;
-  int64_t ld_r, ld_o;
+  int64_t ld_r, ld_o, lo_stride;
   uint32_t *err;
 };
 
@@ -72,7 +73,8 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-template <bool GATED>
+// U: tokens a thread joins at a time
+template <bool GATED, int U>
 __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_constant__ FewParams P) {
   using T = __nv_bfloat16;
   constexpr int NW = GATED ? 2 : 1;                // weight tiles of a stage
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
   __shared__ uint64_t s_limit_sh;
 
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const uint32_t x_bytes = (uint32_t)P.tt * BK * 2, stage_bytes = NW * kWBytes + x_bytes;
+  const uint32_t x_bytes = (uint32_t)P.tt * BK * 2, stage_bytes = NW * kWBytes + P.planes * x_bytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = P.split, rank = (int)(blockIdx.x % (unsigned)split);
   const int n0 = (int)(blockIdx.x / (unsigned)split) * BN;
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
       mbar_expect_tx(&full_bar[stage], stage_bytes);
       tma_load_3d(s0, &P.w, fb, kb * BK, n0, 0);
       if (GATED) tma_load_3d(s0 + kWBytes, &P.w3, fb, kb * BK, n0, 0);
-      tma_load_3d(s0 + NW * kWBytes, &P.x, fb, kb * BK, (int)t0, 0);
+      tma_load_3d(s0 + NW * kWBytes, &P.x, fb, kb * BK, (int)t0, 0);           // all planes
       if (++stage == P.stages) { stage = 0; phase ^= 1u; }
     }
     // aborting: the last round of each stage has to land before the exit
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
       for (int i = kb - 1, n = 0; i >= kb0 && n < P.stages; --i, ++n)
         mbar_wait_drain(&full_bar[(i - kb0) % P.stages], (uint32_t)((i - kb0) / P.stages) & 1u);
   } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_bf16(BN, P.tt);
+    const uint32_t idesc = idesc_bf16(BN, P.planes * P.tt);
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
@@ -185,6 +187,13 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
       uint32_t r[16];
       tmem_ld16(ta + c, r);
       tmem_ld_wait();
+      if (!GATED && P.planes == 2) {
+        uint32_t lo[16];
+        tmem_ld16(ta + P.tt + c, lo);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(lo[i]));
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) part[(c + i) * BN + row] = kb1 > kb0 ? __uint_as_float(r[i]) : 0.0f;
     }
@@ -199,11 +208,16 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
     const float b3 = GATED && in && P.bias3 ? to_f32(static_cast<const T *>(P.bias3)[n]) : 0.0f;
     const int nt = (int)min((int64_t)P.tt, P.M - t0);
     const uint32_t p0 = smem0 + 4u * row, m3 = (uint32_t)P.tt * BN * 4;
-    // U tokens at a time, the partials of four ranks in flight for each,
+    // U tokens at a time, with everything they read in flight (a token past the
+    // last one reads the last one again); partials of four ranks at a time,
     // added in rank order
-    constexpr int U = GATED ? 2 : 4;
     for (int t = 2 * rank + tid / BN; t < nt; t += U * step) {
-      float v[U] = {}, u[U] = {};
+      float v[U] = {}, u[U] = {}, res[U] = {};
+      if (!GATED && P.residual && in) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          res[i] = to_f32(static_cast<const T *>(P.residual)[(t0 + min(t + i * step, nt - 1)) * P.ld_r + n]);
+      }
       for (int r = 0; r < split; r += 4) {
         float pv[4][U], pu[4][U];
 #pragma unroll
@@ -228,22 +242,33 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
         }
       }
       if (!in) continue;
+      const int live = (nt - 1 - t) / step + 1;               // tokens of these U that exist
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (t + i * step >= nt) break;
-        const int64_t m = t0 + t + i * step;
-        float y = v[i] + b;
-        if (P.pre) from_f32(static_cast<T *>(P.pre)[m * P.N + n], y);
-        with_act(P.act, [&](auto A) { y = act_fwd<true, decltype(A)::value>(y); });
-        if (GATED) {
-          const float w = u[i] + b3;
-          if (P.pre3) from_f32(static_cast<T *>(P.pre3)[m * P.N + n], w);
-          y *= w;
-        } else if (P.residual) {
-          y += to_f32(static_cast<const T *>(P.residual)[m * P.ld_r + n]);
-        }
-        from_f32(static_cast<T *>(P.out)[m * P.ld_o + n], y);
+        v[i] += b;
+        if (GATED) u[i] += b3;
       }
+      if (P.pre) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (i < live) {
+            const int64_t at = (t0 + t + i * step) * P.N + n;
+            from_f32(static_cast<T *>(P.pre)[at], v[i]);
+            if (GATED && P.pre3) from_f32(static_cast<T *>(P.pre3)[at], u[i]);
+          }
+      }
+      with_act(P.act, [&](auto A) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[i] = act_fwd<true, decltype(A)::value>(v[i]);
+      });
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (i < live) {
+          T *o = static_cast<T *>(P.out) + (t0 + t + i * step) * P.ld_o + n;
+          const float y = GATED ? v[i] * u[i] : v[i] + res[i];
+          from_f32(*o, y);
+          if (P.lo_stride) from_f32(o[P.lo_stride], y - to_f32(*o));
+        }
     }
   }
   cluster_sync_all();              // no CTA leaves while another may read its partial tile
@@ -266,9 +291,9 @@ cudaError_t allow_smem() {
   return e;
 }
 
-template <bool GATED>
+template <bool GATED, int U>
 cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, size_t smem, cudaStream_t s) {
-  constexpr auto kern = dense_few_kernel<GATED>;
+  constexpr auto kern = dense_few_kernel<GATED, U>;
   cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -295,7 +320,8 @@ cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, s
 // N = 4096: 15.7 against 30 at 128; gated 84 against 129 (64), 101 against 128 (128).
 constexpr int64_t kFewRows = 128;
 bool dense_few_ok(const DenseGemm &g) {
-  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.dtype == MOE_BF16 && g.M <= kFewRows && dense_tc_ok(g);
+  return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.dtype == MOE_BF16 && g.M <= kFewRows &&
+         (g.a.planes < 2 || (g.epi == kDenseLinear && g.M <= 128 / 2)) && g.b.planes < 2 && g.b3.planes < 2 && dense_tc_ok(g);
 }
 
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {
@@ -303,7 +329,8 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   const int nw = gated ? 2 : 1;
   FewParams P{};
   P.tt = (int)std::min<int64_t>(128, (g.M + 15) / 16 * 16);
-  const size_t stage = (size_t)nw * kWBytes + (size_t)P.tt * BK * 2;
+  P.planes = std::max(1, g.a.planes);
+  const size_t stage = (size_t)nw * kWBytes + (size_t)P.planes * P.tt * BK * 2;
   // CTAs an SM and CTAs a tile: what keeps most bytes in flight.  A CTA has at
   // least two stages and six k-blocks; clusters of 1, 2, 4 or 8 (clusters of 3 fitted the SMs
   // badly: 88 us where 4 took 65, one row of a 5120 / 12288 gated block; 2 took
@@ -311,17 +338,18 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.KB = (int)((g.K + BK - 1) / BK);
   const int64_t tiles = (g.N + BN - 1) / BN, ttiles = (g.M + P.tt - 1) / P.tt;
   const size_t partial = (size_t)nw * P.tt * BN * 4;
+  const int cols = P.planes * nw * P.tt;                     // of the accumulators
   double best = 0;
   for (int per_sm = 1; per_sm <= 4; ++per_sm) {
     const size_t room = kMaxSmem / per_sm - (per_sm > 1 ? 2048 : 1024);       // stages or partial tile of a CTA
     const int stages = (int)std::min<size_t>(kMaxStages, room / stage);
-    if (stages < 2 || partial > room || per_sm * nw * std::max(32, P.tt) > 512) continue;
+    if (stages < 2 || partial > room || per_sm * std::max(32, cols) > 512) continue;
     int split = 1;
     while (split < 8 && tiles * ttiles * split * 2 <= (int64_t)device_sms() * per_sm && P.KB / (split * 2) >= 6)
       split *= 2;
     // (one CTA an SM leaves the next kernel's no room to start beside it)
     const double flight = (double)std::min<int64_t>(tiles * ttiles * split, (int64_t)device_sms() * per_sm) * stages *
-                          (per_sm == 1 ? 0.75 : 1.0);
+                          (per_sm == 1 ? 0.6 : 1.0);
     if (flight >= best) {
       best = flight;
       P.stages = stages;
@@ -329,14 +357,14 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
     }
   }
   P.tmem_cols = 32;
-  while (P.tmem_cols < nw * P.tt) P.tmem_cols *= 2;
+  while (P.tmem_cols < cols) P.tmem_cols *= 2;
   const size_t smem = 1024 + std::max(P.stages * stage, (size_t)nw * P.tt * BN * 4);
-  if (!make_map3d(&P.x, g.a.p, g.K, g.M, 1, g.M == 1 ? (g.K + 7) / 8 * 8 : g.a.rs,
-                  (g.M == 1 ? (g.K + 7) / 8 * 8 : g.a.rs) * g.M, P.tt) ||
-      !make_map3d(&P.w, g.b.p, g.K, g.N, 1, g.N == 1 ? (g.K + 7) / 8 * 8 : g.b.rs,
-                  (g.N == 1 ? (g.K + 7) / 8 * 8 : g.b.rs) * g.N, BN) ||
-      (gated && !make_map3d(&P.w3, g.b3.p, g.K, g.N, 1, g.N == 1 ? (g.K + 7) / 8 * 8 : g.b3.rs,
-                            (g.N == 1 ? (g.K + 7) / 8 * 8 : g.b3.rs) * g.N, BN)))
+  auto map = [&](CUtensorMap *m, const Operand &o, int64_t rows, int box) {
+    const int64_t ld = rows == 1 ? pack_ld(g.K) : o.rs;
+    return make_map3d(m, o.p, g.K, rows, std::max(1, o.planes), ld, o.planes > 1 ? o.plane_stride : ld * rows, box,
+                      std::max(1, o.planes));
+  };
+  if (!map(&P.x, g.a, g.M, P.tt) || !map(&P.w, g.b, g.N, BN) || (gated && !map(&P.w3, g.b3, g.N, BN)))
     return cudaErrorInvalidValue;
   P.M = g.M;
   P.N = g.N;
@@ -349,9 +377,14 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.pre3 = g.pre3;
   P.ld_r = g.ld_r;
   P.ld_o = g.ld_o;
+  P.lo_stride = g.lo_stride;
   P.err = err;
-  return gated ? launch_few_as<true>(P, (unsigned)tiles, (unsigned)ttiles, smem, s)
-               : launch_few_as<false>(P, (unsigned)tiles, (unsigned)ttiles, smem, s);
+  // more tokens at a time hide more latency, and cost a thread with one of them
+  // idle loads
+  const unsigned nt = (unsigned)tiles, tt = (unsigned)ttiles;
+  if (g.M <= 2 * P.split)
+    return gated ? launch_few_as<true, 1>(P, nt, tt, smem, s) : launch_few_as<false, 1>(P, nt, tt, smem, s);
+  return gated ? launch_few_as<true, 4>(P, nt, tt, smem, s) : launch_few_as<false, 8>(P, nt, tt, smem, s);
 }
 
 }  // namespace moe

@@ -11,7 +11,9 @@ namespace moe {
 // (strides in elements).  ks == 1: the contraction index is contiguous
 // (K-major); rs == 1: the rows are (MN-major).
 // planes: bf16 matrices plane_stride elements apart whose sum is the operand
-// (0: p has the product's own dtype)
+// (0: p has the product's own dtype).  Three for the tensor cores' copy of an
+// fp32 matrix; two (the value rounded, and the rest rounded) for what a bf16
+// call of few rows hands from one of its products to the next.
 struct Operand {
   const void *p;
   int64_t rs, ks;
@@ -41,6 +43,7 @@ struct DenseGemm {
   int64_t ld_r;
   void *out;                     // [M] rows, ld_o apart
   int64_t ld_o;
+  int64_t lo_stride;             // not 0: out, out2, out3 are two planes this far apart
   void *pre, *pre3;              // [M, N] packed, or null
   const void *pre_in, *pre3_in;  // [M, N] packed
   void *out2, *out3;             // rows ld_o apart
@@ -64,7 +67,7 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
 // `inner` elements, ld apart, into bf16 planes of round_up(inner, 8) elements a
 // line: one plane (bf16, to align the lines) or the three planes of an fp32
 // matrix.  Up to kMaxPack matrices in one launch.
-constexpr int kMaxPack = 6;
+constexpr int kMaxPack = 8;
 struct PackJob {
   const void *src;
   int64_t lines, inner, ld;
@@ -93,11 +96,11 @@ cudaError_t launch_dense_rows(const DenseGemm &g, cudaStream_t s);
 constexpr int kMaxColSums = 3;
 struct ColSum {
   const void *src;
-  int64_t ld;
+  int64_t ld, src_lo;            // src_lo not 0: src is two planes this far apart
   int N;
   const void *z;
   void *dz;
-  int64_t ld_dz;
+  int64_t ld_dz, lo_stride;      // lo_stride not 0: dz is two planes this far apart
   void *out;
 };
 size_t colsum_scratch(int64_t M, int N, int count);

@@ -75,6 +75,12 @@ __global__ void __launch_bounds__(32 * kWarps) dense_rows_kernel(const DenseGemm
     for (int m = 0; m < MT; ++m) {
       float v[V];
       load_k<T, VEC>(xr[m], k, k1, v);
+      if (P.a.planes == 2) {
+        float lo[V];
+        load_k<T, VEC>(xr[m] + P.a.plane_stride, k, k1, lo);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] += lo[j];
+      }
 #pragma unroll
       for (int r = 0; r < kRows; ++r)
 #pragma unroll
@@ -111,7 +117,9 @@ __global__ void __launch_bounds__(32 * kWarps) dense_rows_kernel(const DenseGemm
     } else if (P.residual) {
       a += to_f32(static_cast<const T *>(P.residual)[row * P.ld_r + n]);
     }
-    from_f32(static_cast<T *>(P.out)[row * P.ld_o + n], a);
+    T *o = static_cast<T *>(P.out) + row * P.ld_o + n;
+    from_f32(*o, a);
+    if (P.lo_stride) from_f32(o[P.lo_stride], a - to_f32(*o));
   }
 }
 
@@ -119,7 +127,7 @@ template <typename T, bool GATED, int MT>
 cudaError_t rows_as(const DenseGemm &g, cudaStream_t s) {
   constexpr int NR = GATED ? kRows / 2 : kRows;
   auto lines16 = [&](const Operand &o) {
-    return !o.p || ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)(o.rs * (int64_t)sizeof(T))) & 15) == 0;
+    return !o.p || ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)((o.rs | o.plane_stride) * (int64_t)sizeof(T))) & 15) == 0;
   };
   const bool vec = lines16(g.a) && lines16(g.b) && lines16(g.b3);
   const int64_t mt = (g.M + MT - 1) / MT, groups = (g.N + NR - 1) / NR;

@@ -40,7 +40,12 @@ struct Slice {
     for (int i = 0; i < N; ++i) {
       int r, k;
       at(o, i, r, k);
-      v[i] = r0 + r < rows && k0 + k < K ? to_f32(p[(r0 + r) * o.rs + (k0 + k) * o.ks]) : 0.0f;
+      v[i] = 0.0f;
+      if (r0 + r < rows && k0 + k < K) {
+        const int64_t e = (r0 + r) * o.rs + (k0 + k) * o.ks;
+        v[i] = to_f32(p[e]);
+        if (o.planes == 2) v[i] += to_f32(p[e + o.plane_stride]);
+      }
     }
   }
   __device__ __forceinline__ void put(const Operand &o, float (*dst)[TS + 1]) const {
@@ -52,6 +57,14 @@ struct Slice {
     }
   }
 };
+
+// v, and what its rounding leaves to the low plane
+template <typename T>
+__device__ __forceinline__ void store_planes(void *base, int64_t at, int64_t lo_stride, float v) {
+  T *p = static_cast<T *>(base) + at;
+  from_f32(*p, v);
+  if (lo_stride) from_f32(p[lo_stride], v - to_f32(*p));
+}
 
 template <typename T>
 __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, float acc, float acc3) {
@@ -75,7 +88,7 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
       if (P.pre3) from_f32(static_cast<T *>(P.pre3)[at], u);
       float f = 0.0f;
       with_act(P.act, [&](auto A) { f = act_fwd<FAST, decltype(A)::value>(a); });
-      from_f32(*out, f * u);
+      store_planes<T>(P.out, m * P.ld_o + n, P.lo_stride, f * u);
       break;
     }
     case kDenseGatedGrad: {
@@ -83,9 +96,9 @@ __device__ __forceinline__ void store1(const DenseGemm &P, int64_t m, int n, flo
       const float u = to_f32(static_cast<const T *>(P.pre3_in)[at]);
       float f = 0.0f, d = 0.0f;
       with_act(P.act, [&](auto A) { act_both<FAST, decltype(A)::value>(a, f, d); });
-      from_f32(*out, acc * u * d);
-      from_f32(static_cast<T *>(P.out2)[m * P.ld_o + n], acc * f);
-      from_f32(static_cast<T *>(P.out3)[m * P.ld_o + n], f * u);
+      store_planes<T>(P.out, m * P.ld_o + n, P.lo_stride, acc * u * d);
+      store_planes<T>(P.out2, m * P.ld_o + n, P.lo_stride, acc * f);
+      store_planes<T>(P.out3, m * P.ld_o + n, P.lo_stride, f * u);
       break;
     }
     default: from_f32(*out, acc);
@@ -212,6 +225,12 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
         if (r + 8 * i >= r1) break;
         float v[V];
         unpack16<T>(a[i], v);
+        if (Q.src_lo) {
+          float lo[V];
+          unpack16<T>(*reinterpret_cast<const uint4 *>(src + Q.src_lo + (r + 8 * i) * Q.ld + n), lo);
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] += lo[j];
+        }
         if (GRAD) {
           float zz[V];
           unpack16<T>(b[i], zz);
@@ -221,7 +240,16 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
             act_both<sizeof(T) == 2, ACT>(zz[j], f, d);
             v[j] *= d;
           }
-          *reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.ld_dz + n) = pack16<T>(v);
+          uint4 *o = reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.ld_dz + n);
+          const uint4 hi = pack16<T>(v);
+          *o = hi;
+          if (Q.lo_stride) {
+            float h[V];
+            unpack16<T>(hi, h);
+#pragma unroll
+            for (int j = 0; j < V; ++j) h[j] = v[j] - h[j];
+            *reinterpret_cast<uint4 *>(dz + Q.lo_stride + (r + 8 * i) * Q.ld_dz + n) = pack16<T>(h);
+          }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) sum[j] += v[j];
@@ -235,11 +263,14 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
         const int c = n0 + 32 * j + lane;
         if (c >= Q.N) break;
         float v = to_f32(src[r * Q.ld + c]);
+        if (Q.src_lo) v += to_f32(src[r * Q.ld + c + Q.src_lo]);
         if (GRAD) {
           float f, d;
           act_both<sizeof(T) == 2, ACT>(to_f32(z[r * Q.N + c]), f, d);
           v *= d;
-          from_f32(dz[r * Q.ld_dz + c], v);
+          T *o = dz + r * Q.ld_dz + c;
+          from_f32(*o, v);
+          if (Q.lo_stride) from_f32(o[Q.lo_stride], v - to_f32(*o));
         }
         sum[j] += v;
       }

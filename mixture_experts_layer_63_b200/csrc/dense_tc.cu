@@ -54,6 +54,11 @@ constexpr int kMaxSegs = 12;
 template <typename T>
 constexpr bool kChunked = sizeof(T) == 4;
 
+// kDenseGatedGrad with outputs in two planes (bf16 calls of very few rows): an
+// instance of its own, the second pass costs the first one registers
+constexpr int kGradPlanes = 16;
+__host__ __device__ constexpr bool is_grad(int epi) { return epi == kDenseGatedGrad || epi == kGradPlanes; }
+
 // A stretch of k-blocks: tensor map and plane (third coordinate) of each operand
 struct Seg {
   uint8_t a, az, b, bz;
@@ -68,7 +73,7 @@ struct TcProblem {
   int32_t tiles_m, tile_end;     // row tiles; tiles of this and the problems before it
   const void *bias, *bias3, *residual, *pre_in, *pre3_in;
   void *out, *pre, *pre3, *out2, *out3;
-  int64_t ld_r, ld_o;
+  int64_t ld_r, ld_o, lo_stride;
 };
 
 struct TcParams {
@@ -283,6 +288,16 @@ __device__ __forceinline__ void store_vals(const Rows<T> &o, int64_t row0, int c
   store_chunk(o, row0, col, w, stg, lane);
 }
 
+// 16 bytes of what rounding v to T leaves
+template <typename T>
+__device__ __forceinline__ uint4 low16(const float *v) {
+  constexpr int E = 16 / sizeof(T);
+  float h[E];
+  unpack16<T>(pack16<T>(v), h);
+#pragma unroll
+  for (int i = 0; i < E; ++i) h[i] = v[i] - h[i];
+  return pack16<T>(h);
+}
 // 16 bytes; the 256-byte stretch around them is brought to L2, where the
 // chunks to come find it
 __device__ __forceinline__ uint4 ld16_ahead(const void *p) {
@@ -352,7 +367,7 @@ template <int EPI, typename T>
 struct Epilogue {
   static constexpr bool FAST = sizeof(T) == 2;
   static constexpr int CW = kCols<T>, E = 16 / sizeof(T);
-  static constexpr int kIn = EPI == kDenseGatedGrad ? 2 : 1;      // matrices read, staging buffers
+  static constexpr int kIn = is_grad(EPI) ? 2 : 1;      // matrices read, staging buffers
   const TcParams &P;
   const TcProblem &Q;
   const int64_t row0;
@@ -370,7 +385,7 @@ struct Epilogue {
     if (row0 >= Q.M || c >= c1) return;
     if (EPI == kDenseLinear && Q.residual)
       in[0].fetch(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col0 + c, lane);
-    if (EPI == kDenseGatedGrad) {
+    if (is_grad(EPI)) {
       in[0].fetch(packed(Q.pre_in), row0, col0 + c, lane);
       in[kIn - 1].fetch(packed(Q.pre3_in), row0, col0 + c, lane);
     }
@@ -428,37 +443,46 @@ struct Epilogue {
       } else {                                           // kDenseGatedGrad
         // a and u staged side by side; dA, dU and h packed piece by piece, so
         // that no more than one matrix is held in fp32
-        uint4 *stg_u = stg + (kIn - 1) * (kStgBytes / 16);
-        in[0].stage(packed(Q.pre_in), row0, col, stg, lane);
-        in[kIn - 1].stage(packed(Q.pre3_in), row0, col, stg_u, lane);
-        __syncwarp();
-        fetch(c + CW);
         acc_cols(taddr + c, v);
-        uint4 da[4], du[4], hh[4];
-        with_act(P.act, [&](auto A) {
+        // low: a pass of its own for the second planes, the parts that the
+        // first one's rounding left (few rows only)
+        auto grads = [&](auto low) {
+          constexpr bool LOW = decltype(low)::value;
+          if (LOW) fetch(c);
+          uint4 *stg_u = stg + (kIn - 1) * (kStgBytes / 16);
+          in[0].stage(packed(Q.pre_in), row0, col, stg, lane);
+          in[kIn - 1].stage(packed(Q.pre3_in), row0, col, stg_u, lane);
+          __syncwarp();
+          fetch(c + CW);
+          uint4 da[4], du[4], hh[4];
+          with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float a[E], u[E], h[E];
-            unpack16<T>(stg[stg_at(lane, k)], a);
-            unpack16<T>(stg_u[stg_at(lane, k)], u);
+            for (int k = 0; k < 4; ++k) {
+              float a[E], u[E], h[E];
+              unpack16<T>(stg[stg_at(lane, k)], a);
+              unpack16<T>(stg_u[stg_at(lane, k)], u);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              float f, d;
-              act_both<FAST, decltype(A)::value>(a[i], f, d);
-              const float dh = v[k * E + i];
-              a[i] = dh * u[i] * d;
-              h[i] = f * u[i];
-              u[i] = dh * f;
+              for (int i = 0; i < E; ++i) {
+                float f, d;
+                act_both<FAST, decltype(A)::value>(a[i], f, d);
+                const float dh = v[k * E + i];
+                a[i] = dh * u[i] * d;
+                h[i] = f * u[i];
+                u[i] = dh * f;
+              }
+              da[k] = LOW ? low16<T>(a) : pack16<T>(a);
+              du[k] = LOW ? low16<T>(u) : pack16<T>(u);
+              hh[k] = LOW ? low16<T>(h) : pack16<T>(h);
             }
-            da[k] = pack16<T>(a);
-            du[k] = pack16<T>(u);
-            hh[k] = pack16<T>(h);
-          }
-        });
-        __syncwarp();
-        store_chunk(out, row0, col, da, stg, lane);
-        store_chunk(Rows<T>(Q.out2, Q.ld_o, Q.M, Q.N), row0, col, du, stg_u, lane);
-        store_chunk(Rows<T>(Q.out3, Q.ld_o, Q.M, Q.N), row0, col, hh, stg, lane);
+          });
+          __syncwarp();
+          const int64_t at = LOW ? Q.lo_stride : 0;
+          store_chunk(Rows<T>(static_cast<T *>(Q.out) + at, Q.ld_o, Q.M, Q.N), row0, col, da, stg, lane);
+          store_chunk(Rows<T>(static_cast<T *>(Q.out2) + at, Q.ld_o, Q.M, Q.N), row0, col, du, stg, lane);
+          store_chunk(Rows<T>(static_cast<T *>(Q.out3) + at, Q.ld_o, Q.M, Q.N), row0, col, hh, stg, lane);
+        };
+        grads(IntC<0>{});
+        if constexpr (EPI == kGradPlanes) grads(IntC<1>{});
       }
     }
   }
@@ -895,28 +919,39 @@ cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
   // 14336: 54.5 us plain, 61 us in pieces).  W is a multiple of the tail's
   // tiles where that leaves each tile at least two pieces (a share that
   // straddles two tiles adds a piece to both).
-  const int tiles = P.pr[P.nprob - 1].tile_end, last = tiles % pairs;
+  // Tiles that take more than about half of a pair's fair share of the whole
+  // launch are in the tail however many they are.
+  const int tiles = P.pr[P.nprob - 1].tile_end;
+  auto steps = [&](int p) { return (int64_t)((P.pr[p].KB + kBks - 1) / kBks) * P.pr[p].segs; };
+  auto begin = [&](int p) { return p ? P.pr[p - 1].tile_end : 0; };
+  int64_t all = 0;
+  for (int p = 0; p < P.nprob; ++p) all += steps(p) * (P.pr[p].tile_end - begin(p));
+  int dp = tiles - tiles % pairs;
+  bool outliers = false;
+  for (int p = P.nprob - 1; p >= 0; --p)
+    if (2 * steps(p) * pairs > all && tiles - begin(p) <= kMaxTail && begin(p) < dp) {
+      dp = begin(p);
+      outliers = true;
+    }
   P.dp_tiles = tiles;
   P.workers = 0;
-  if (last > 0 && P.part) {
-    const int dp = tiles - last;
-    int64_t total = 0;
-    int deepest = 0;
+  if (dp < tiles && P.part) {
+    const int last = tiles - dp;
+    int64_t total = 0, deepest = 0;
     for (int p = 0; p < P.nprob; ++p) {
-      const int begin = std::max(dp, p ? P.pr[p - 1].tile_end : 0), n = std::max(0, P.pr[p].tile_end - begin);
-      const int steps = (P.pr[p].KB + kBks - 1) / kBks * P.pr[p].segs;
-      P.tail_tile[p] = begin;
+      const int from = std::max(dp, begin(p)), n = std::max(0, P.pr[p].tile_end - from);
+      P.tail_tile[p] = from;
       P.tail_step[p] = total;
-      total += (int64_t)n * steps;
-      if (n) deepest = std::max(deepest, steps);
+      total += n * steps(p);
+      if (n) deepest = std::max(deepest, steps(p));
     }
     P.tail_step[P.nprob] = total;
     // at least kMinSteps a worker, at most kMaxPieces pieces a tile
     const int64_t least = std::max<int64_t>(kMinSteps, (deepest + kMaxPieces - 3) / (kMaxPieces - 2));
     int workers = (int)std::min<int64_t>(pairs, total / least);
     if (workers >= 2 * last) workers -= workers % last;
-    if (workers > 0 &&
-        (double)total / workers + kJoinSteps + 2.0 * deepest * workers / total < (double)deepest) {
+    const double plain = outliers ? (double)std::max(deepest, total / pairs) : (double)deepest;
+    if (workers > 0 && (double)total / workers + kJoinSteps + 2.0 * deepest * workers / total < plain) {
       P.dp_tiles = dp;
       P.workers = workers;
     }
@@ -932,7 +967,10 @@ cudaError_t launch_as(int epi, TcParams &P, cudaStream_t s) {
   switch (epi) {
     case kDenseLinear: return launch_pair_as<kDenseLinear, T>(P, s);
     case kDenseGated: return launch_pair_as<kDenseGated, T>(P, s);
-    case kDenseGatedGrad: return launch_pair_as<kDenseGatedGrad, T>(P, s);
+    case kDenseGatedGrad:
+      if constexpr (sizeof(T) == 2)
+        if (P.pr[0].lo_stride) return launch_pair_as<kGradPlanes, T>(P, s);
+      return launch_pair_as<kDenseGatedGrad, T>(P, s);
     default: return launch_pair_as<kDenseStore, T>(P, s);
   }
 }
@@ -963,11 +1001,11 @@ constexpr uint8_t kPlanePairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {
 
 bool dense_tc_ok(const DenseGemm &g) {
   if (g.K < 1 || g.M < 1 || g.M > 0x7ffffe00 || g.K > 0x7ffffe00 || g.N > 0x7ffffe00) return false;
-  const int planes = g.dtype == MOE_F32 ? 3 : 0;
+  const bool f32 = g.dtype == MOE_F32;
   for (const Operand *o : {&g.b, &g.b3, &g.b2})
-    if (o->p && (!tma_ok(*o, g.N, g.K) || (planes == 3) != (o->planes == 3))) return false;
+    if (o->p && (!tma_ok(*o, g.N, g.K) || o->planes > (f32 ? 3 : 2) || f32 != (o->planes == 3))) return false;
   for (const Operand *o : {&g.a, &g.a2})
-    if (o->p && (!tma_ok(*o, g.M, g.K) || (planes == 3) != (o->planes == 3))) return false;
+    if (o->p && (!tma_ok(*o, g.M, g.K) || f32 != (o->planes == 3))) return false;
   return (!g.a2.p || (kmajor(g.a) == kmajor(g.a2) && kmajor(g.b) == kmajor(g.b2))) &&
          (!g.b3.p || kmajor(g.b) == kmajor(g.b3)) && (g.epi != kDenseGated || kmajor(g.b));
 }
@@ -1014,10 +1052,15 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
            map_operand(&Q.b[1], G.b2, G.N, G.K, box_b(G.b2));
     if (G.b3.p) ok = ok && map_operand(&Q.b[1], G.b3, G.N, G.K, box_b(G.b3));
     if (!ok) return cudaErrorInvalidValue;
-    const int pairs_of_planes = G.dtype == MOE_F32 ? 6 : 1;
-    for (int q = 0; q < pairs_of_planes; ++q)
-      for (uint8_t i = 0; i < (G.a2.p ? 2 : 1); ++i)
-        Q.seg[Q.segs++] = pairs_of_planes == 1 ? Seg{i, 0, i, 0} : Seg{i, kPlanePairs[q][0], i, kPlanePairs[q][1]};
+    // segments, smallest products first
+    auto segments = [&](uint8_t az, uint8_t bz) {
+      for (uint8_t i = 0; i < (G.a2.p ? 2 : 1); ++i) Q.seg[Q.segs++] = {i, az, i, bz};
+    };
+    if (G.dtype == MOE_F32)
+      for (const auto &q : kPlanePairs) segments(q[0], q[1]);
+    else
+      for (int az = std::max(1, G.a.planes) - 1; az >= 0; --az)
+        for (int bz = std::max(1, G.b.planes) - 1; bz >= 0; --bz) segments((uint8_t)az, (uint8_t)bz);
     Q.amn = !kmajor(G.a);
     Q.bmn = !kmajor(G.b);
     Q.M = G.M;
@@ -1031,6 +1074,7 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
     Q.ld_r = G.ld_r;
     Q.out = G.out;
     Q.ld_o = G.ld_o;
+    Q.lo_stride = G.lo_stride;
     Q.pre = G.pre;
     Q.pre3 = G.pre3;
     Q.pre_in = G.pre_in;

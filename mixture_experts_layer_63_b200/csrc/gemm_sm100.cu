@@ -1939,12 +1939,12 @@ bool make_map_f32(CUtensorMap *m, const void *base, uint64_t inner, uint64_t out
 }
 
 bool make_map3d(CUtensorMap *m, const void *base, int64_t inner, int64_t lines, int64_t planes, int64_t ld,
-                int64_t plane_stride, uint32_t box) {
+                int64_t plane_stride, uint32_t box, uint32_t box_planes) {
   EncodeTiledFn enc = encode_fn();
   if (!enc || inner < 1 || lines < 1 || planes < 1) return false;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)lines, (cuuint64_t)planes};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)plane_stride * 2};
-  cuuint32_t boxd[3] = {(cuuint32_t)BK, box, 1};
+  cuuint32_t boxd[3] = {(cuuint32_t)BK, box, box_planes};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, boxd,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

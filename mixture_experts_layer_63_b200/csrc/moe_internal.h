@@ -278,9 +278,9 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer,
               uint32_t box_outer);
 int device_sms();
 // 3-D bf16 map {inner, lines, planes} (ld and plane_stride in elements) in
-// boxes of 64 inner elements x `box` lines x 1 plane, 128-byte swizzle
+// boxes of 64 inner elements x `box` lines x box_planes planes, 128-byte swizzle
 bool make_map3d(CUtensorMap *m, const void *base, int64_t inner, int64_t lines, int64_t planes, int64_t ld,
-                int64_t plane_stride, uint32_t box);
+                int64_t plane_stride, uint32_t box, uint32_t box_planes = 1);
 
 // --- router GEMM with the gate in its epilogue (router_tc.cu) ---------------
 // true when moe_route / moe_forward run the bf16 router through it
