@@ -360,9 +360,18 @@ MOE_API moe_status moe_backward(const moe_config *cfg, const void *x, const void
  *     only.  Rows whose base address and stride are multiples of 16 bytes
  *     are read fastest;
  *   - biases, residuals and gradients have the layer's dtype.  Sums are held
- *     in fp32 and each output is rounded once; the intermediate matrices
- *     that a second product reads (h; in the backward passes dz, dA, dU and
- *     the remade h) are rounded to the layer's dtype first;
+ *     in fp32 and each output is rounded once.  bf16: the intermediate
+ *     matrices that a second product reads (h; in the backward passes dz, dA,
+ *     dU and the remade h) are rounded to bf16 first (to 16 significant bits
+ *     in calls of at most 16 rows, 4 backward);
+ *   - fp32: products run in fp32, or on the tensor cores with each operand
+ *     split exactly into three bf16 parts (an error of 2e-7 of the result's
+ *     norm, below an fp32 product's own).  There an infinite element gives
+ *     NaN where fp32 arithmetic would give an infinity, and elements below
+ *     2^-108 lose low bits;
+ *   - a workspace serves one call at a time, of any of these entry points that
+ *     it is large enough for; its 4 KiB control block must have been cleared
+ *     once (moe_workspace_init);
  *   - outputs may not overlap inputs or one another, except that y may be
  *     the residual itself (same address and stride).  Column slices of one
  *     wider buffer do not overlap.

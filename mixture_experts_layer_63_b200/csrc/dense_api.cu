@@ -120,6 +120,11 @@ int planes_of(int dtype, int64_t rows, bool backward) {
   return dtype == MOE_BF16 && rows <= (backward ? 4 : 16) ? 2 : 1;
 }
 
+// Room for cut tiles (dense_tc.cu): forward calls of few rows never get there
+size_t tail_room(int dtype, int64_t rows, bool backward) {
+  return !backward && rows <= (dtype == MOE_F32 ? kRegisterRows : kFewRows) ? 0 : dense_tail_bytes();
+}
+
 struct LinearLayout {
   size_t dz, part, tail, pack, total;
 };
@@ -134,7 +139,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
     L.part = t.take(colsum_scratch(c.M, c.N, 1));
     room += pack_room(c.dtype, c.M, c.N, act ? pack_ld(c.N) : c.ld_y);
   }
-  L.tail = t.take(dense_tail_bytes());
+  L.tail = t.take(tail_room(c.dtype, c.M, backward));
   L.pack = t.take(room);
   L.total = t.o;
   return L;
@@ -146,7 +151,7 @@ LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
 class Products {
  public:
   Products(int dtype, void *ws, size_t tail, size_t pack, size_t end, cudaStream_t s)
-      : dtype_(dtype), base_(static_cast<char *>(ws)), tail_(tail), at_(pack), end_(end), s_(s) {}
+      : dtype_(dtype), base_(static_cast<char *>(ws)), tail_(tail), first_(pack), at_(pack), end_(end), s_(s) {}
 
   cudaError_t run(DenseGemm *g, int n) {
     uint32_t *err = reinterpret_cast<uint32_t *>(base_);
@@ -174,7 +179,7 @@ class Products {
         launched_ = jobs_;
         if (e != cudaSuccess) return e;
         if (n == 1 && dense_few_ok(q[0])) return launch_dense_few(q[0], err, s_);
-        return launch_dense_tc(q, n, err, reinterpret_cast<float *>(base_ + tail_), s_);
+        return launch_dense_tc(q, n, err, tail_ < first_ ? reinterpret_cast<float *>(base_ + tail_) : nullptr, s_);
       }
       jobs_ = launched_;
     }
@@ -220,7 +225,7 @@ class Products {
 
   int dtype_;
   char *base_;
-  size_t tail_, at_, end_;
+  size_t tail_, first_, at_, end_;        // cut tiles; copies: their first, next and last byte
   cudaStream_t s_;
   PackJob job_[kMaxJobs];
   int jobs_ = 0, launched_ = 0;
@@ -282,7 +287,7 @@ GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
     L.part = t.take(colsum_scratch(T, std::max(c.d_ff, c.d_model), 3));
     pack += 2 * room(T, f, ldh) + room(T, d, c.ld_y);
   }
-  L.tail = t.take(dense_tail_bytes());
+  L.tail = t.take(tail_room(c.dtype, T, backward));
   L.pack = t.take(pack);
   L.total = t.o;
   return L;

@@ -315,13 +315,9 @@ cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, s
 
 }  // namespace
 
-// One tile of tokens.  Against 256-row tiles (dense_tc.cu), K = 4096, N = 14336:
-// 27.5 us against 32.0 at 64 rows, 32.7 against 32.7 at 128, 48 against 34 at 192;
-// N = 4096: 15.7 against 30 at 128; gated 84 against 129 (64), 101 against 128 (128).
-constexpr int64_t kFewRows = 128;
 bool dense_few_ok(const DenseGemm &g) {
   return (g.epi == kDenseLinear || g.epi == kDenseGated) && g.dtype == MOE_BF16 && g.M <= kFewRows &&
-         (g.a.planes < 2 || (g.epi == kDenseLinear && g.M <= 128 / 2)) && g.b.planes < 2 && g.b3.planes < 2 && dense_tc_ok(g);
+         (g.a.planes < 2 || (g.epi == kDenseLinear && 2 * g.M <= kFewRows)) && g.b.planes < 2 && g.b3.planes < 2 && dense_tc_ok(g);
 }
 
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {

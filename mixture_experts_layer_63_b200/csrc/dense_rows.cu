@@ -155,7 +155,7 @@ cudaError_t rows_of(const DenseGemm &g, cudaStream_t s) {
 bool dense_rows_ok(const DenseGemm &g) {
   if (g.epi != kDenseLinear && g.epi != kDenseGated) return false;
   const bool small = g.K * g.N <= (int64_t)1 << 21;
-  return g.M <= (g.dtype == MOE_F32 ? (small ? 32 : 16) : (small ? 8 : 2));
+  return g.M <= (g.dtype == MOE_F32 ? (small ? 2 * kRegisterRows : kRegisterRows) : (small ? 8 : 2));
 }
 
 cudaError_t launch_dense_rows(const DenseGemm &g, cudaStream_t s) {

@@ -522,6 +522,62 @@ def test_two_streams_with_their_own_workspaces():
     assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
 
 
+def test_one_workspace_serves_different_calls_in_turn():
+    """Cut tiles, copies and partial sums of one call leave nothing that the
+    next call on the workspace reads."""
+    g = gen(14)
+    dtype = BF16
+    lc, gc = api.linear_config(300, 8200, 520, "gelu"), api.gated_ffn_config(700, 264, 200)
+    n = max(api.new_linear_workspace(lc, backward=True).numel(), api.new_gated_ffn_workspace(gc, backward=True).numel())
+    shared = torch.randint(0, 255, (n,), dtype=torch.uint8, device="cuda")
+    api.moe_workspace_init(shared)
+    x, w, z, dy = (rnd(g, *s, dtype=dtype, std=0.3) for s in ((300, 8200), (520, 8200), (300, 520), (300, 520)))
+    gx, w1, w3, w2 = (rnd(g, *s, dtype=dtype, std=0.1) for s in ((700, 264), (200, 264), (200, 264), (264, 200)))
+    got = []
+    for ws in (None, shared, shared):
+        o = [torch.empty(s, dtype=dtype, device="cuda") for s in ((300, 520), (300, 8200), (520, 8200), (520,), (700, 264))]
+        api.moe_linear(lc, x, w, None, None, o[0], None, api.new_linear_workspace(lc) if ws is None else ws)
+        api.moe_gated_ffn(gc, gx, w1, None, w3, None, w2, None, gx, o[4], None, None,
+                          api.new_gated_ffn_workspace(gc) if ws is None else ws)
+        api.moe_linear_backward(lc, x, w, z, dy, o[1], o[2], o[3],
+                                api.new_linear_workspace(lc, backward=True) if ws is None else ws)
+        torch.cuda.synchronize()
+        got.append(o)
+    api.moe_check_device_errors(shared)
+    for o in got[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(got[0], o))
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_fp32_extremes(M):
+    """Huge and tiny fp32 values (beyond bf16's rounding range and next to its
+    smallest): the split into bf16 parts keeps them; an infinite element makes
+    its row's results non-finite and leaves the others alone."""
+    g = gen(15)
+    K, N = 640, 200
+    w = rnd(g, N, K, dtype=F32, std=1.0)
+    cfg = api.linear_config(M, K, N, dtype=F32)
+    ws = api.new_linear_workspace(cfg)
+    for scale in (1e30, 1e-20):
+        x = rnd(g, M, K, dtype=F32, std=scale)
+        y = torch.empty(M, N, device="cuda")
+        api.moe_linear(cfg, x, w, None, None, y, None, ws)
+        ref = x.double() @ w.double().T
+        near(y, ref, ck(K) * (x.double().abs() @ w.double().abs().T), f"scale {scale}")
+    x = rnd(g, M, K, dtype=F32)
+    x[0, 0] = 3.4e38                               # rounds to infinity in bf16
+    w2 = w * 1e-3
+    api.moe_linear(cfg, x, w2, None, None, y, None, ws)
+    near(y, x.double() @ w2.double().T, ck(K) * (x.double().abs() @ w2.double().abs().T), "next to the largest")
+    x[1, 5] = math.inf
+    y2 = torch.empty_like(y)
+    api.moe_linear(cfg, x, w2, None, None, y2, None, ws)
+    torch.cuda.synchronize()
+    assert not y2[1].isfinite().any()
+    keep = torch.arange(M, device="cuda") != 1
+    assert torch.equal(y[keep], y2[keep])
+
+
 def test_binding_refuses_wrong_tensors():
     cfg = api.linear_config(8, 16, 24)
     ws = api.new_linear_workspace(cfg)
