@@ -514,6 +514,50 @@ __device__ __forceinline__ int group_col(int bnh, int cols, int half, int i) {
   return c < w && half * w + c < cols ? g * bnh + half * w + c : -1;
 }
 
+// fp32: the accumulators of a piece's chunks, one after another, into a sum in
+// registers, which takes the last one's place in TMEM at the end.  Returns the
+// accumulator it is in (bit 0) and its phase (bit 1), -1 after a wait that ran
+// out.  A call of its own: the sum takes 128 registers, and what the caller
+// keeps is spilled once a tile instead of once a chunk.
+struct ChunkWaits {
+  uint64_t *full;
+  uint32_t empty0, empty1;           // the even CTA's
+  volatile int *abort;
+  uint32_t *err;
+  uint64_t limit;
+};
+template <int EPI>
+__device__ __noinline__ int sum_chunks(const ChunkWaits w, uint32_t tmem, int bnh, int cols, int half, int chunks,
+                                       int acc, uint32_t phase) {
+  float sum[4][32] = {};
+  for (int c = 0;; ++c) {
+    if (!__all_sync(0xffffffffu, mbar_wait(w.full + acc, phase, w.abort, w.err, w.limit))) return -1;
+    tc_fence_after();
+    const uint32_t ta = tmem + (uint32_t)(acc * kAccCols);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = group_col<EPI>(bnh, cols, half, i);
+      if (col >= 0) {
+        uint32_t r[32];
+        tmem_ld32(ta + col, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(r[j]);
+        if (c + 1 == chunks) tmem_st32(ta + col, sum[i]);
+      }
+    }
+    if (c + 1 == chunks) break;
+    tc_fence_before();
+    mbar_arrive_cluster(acc ? w.empty1 : w.empty0);
+    if (++acc == 2) {
+      acc = 0;
+      phase ^= 1u;
+    }
+  }
+  tmem_st_wait();
+  return acc | (int)(phase << 1);
+}
+
 // A piece that is not the whole tile: this warp's part of the accumulator to
 // the piece's slot, then a count of the pieces that are there.  The warp that
 // finds itself last adds the tile's pieces in order, puts the sum in TMEM and
@@ -809,32 +853,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!kChunked<T> && pc.whole()) ep.begin();
       bool ok = true;
       if (kChunked<T>) {
-        // all chunks but the last join the sum in registers; the last one's
-        // place in TMEM then takes the whole sum
-        float sum[4][32] = {};
         const int chunks = (pc.s1 - 1) / Q.segs - pc.s0 / Q.segs + 1;
-        for (int c = 0; c < chunks; ++c) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&accf_bar[acc], acc_phase, &s_abort, P.err, s_limit)))) break;
-          tc_fence_after();
-          const uint32_t ta = tmem_base + (uint32_t)(acc * kAccCols) + lanes;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int col = group_col<EPI>(P.bnh, Q.N - col0, half, i);
-            if (col < 0) continue;
-            uint32_t r[32];
-            tmem_ld32(ta + col, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[i][j] += __uint_as_float(r[j]);
-            if (c + 1 == chunks) tmem_st32(ta + col, sum[i]);
-          }
-          if (c + 1 == chunks) break;
-          tc_fence_before();
-          mbar_arrive_cluster(acce_even[acc]);
-          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
-        }
+        const ChunkWaits cw{accf_bar, acce_even[0], acce_even[1], &s_abort, P.err, s_limit};
+        const int at = sum_chunks<EPI>(cw, tmem_base + lanes, P.bnh, Q.N - col0, half, chunks, acc, acc_phase);
+        ok = at >= 0;
         if (ok) {
-          tmem_st_wait();
+          acc = at & 1;
+          acc_phase = (uint32_t)at >> 1;
           if (pc.whole()) ep.begin();
         }
       } else {
