@@ -22,13 +22,22 @@ constexpr int kWarps = 8;
 constexpr int kRows = 4;               // rows of W a warp (gated: two of W1, the same two of W3)
 
 // V consecutive elements (VEC), or the V elements 32 apart that a lane owns
-template <typename T, bool VEC>
+// STREAM: without a place in L1 (the weights; x stays there)
+template <typename T, bool VEC, bool STREAM>
 __device__ __forceinline__ void load_k(const T *p, int64_t k, int64_t K, float (&v)[16 / sizeof(T)]) {
   constexpr int V = 16 / sizeof(T);
   const int lane = threadIdx.x % 32;
   if (VEC) {
     if (k + (lane + 1) * V <= K) {
-      unpack16<T>(__ldg(reinterpret_cast<const uint4 *>(p + k) + lane), v);
+      const uint4 *q = reinterpret_cast<const uint4 *>(p + k) + lane;
+      uint4 w;
+      if (STREAM)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "l"(q));
+      else
+        w = __ldg(q);
+      unpack16<T>(w, v);
       return;
     }
 #pragma unroll
@@ -39,7 +48,8 @@ __device__ __forceinline__ void load_k(const T *p, int64_t k, int64_t K, float (
   }
 }
 
-template <typename T, bool GATED, int MT, bool VEC>
+// PLANES: x is two planes (bf16)
+template <typename T, bool GATED, int MT, bool VEC, bool PLANES>
 __global__ void __launch_bounds__(32 * kWarps) dense_rows_kernel(const DenseGemm P, int ks) {
   constexpr int V = 16 / sizeof(T), NR = GATED ? kRows / 2 : kRows;
   constexpr bool FAST = sizeof(T) == 2;
@@ -70,14 +80,14 @@ __global__ void __launch_bounds__(32 * kWarps) dense_rows_kernel(const DenseGemm
   for (int64_t k = k0; k < k1; k += step) {
     float w[kRows][V];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) load_k<T, VEC>(wr[r], k, k1, w[r]);
+    for (int r = 0; r < kRows; ++r) load_k<T, VEC, true>(wr[r], k, k1, w[r]);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float v[V];
-      load_k<T, VEC>(xr[m], k, k1, v);
-      if (P.a.planes == 2) {
+      load_k<T, VEC, false>(xr[m], k, k1, v);
+      if (PLANES) {
         float lo[V];
-        load_k<T, VEC>(xr[m] + P.a.plane_stride, k, k1, lo);
+        load_k<T, VEC, false>(xr[m] + P.a.plane_stride, k, k1, lo);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] += lo[j];
       }
@@ -135,8 +145,11 @@ cudaError_t rows_as(const DenseGemm &g, cudaStream_t s) {
   int ks = 1;
   while (ks < kWarps && blocks(ks) < (int64_t)device_sms() * 4 && g.K / (2 * ks) >= 512) ks *= 2;
   if (blocks(ks) > 0x7fffffff) return cudaErrorInvalidValue;
-  return vec ? launch_kernel(dense_rows_kernel<T, GATED, MT, true>, (unsigned)blocks(ks), 32 * kWarps, 0, s, g, ks)
-             : launch_kernel(dense_rows_kernel<T, GATED, MT, false>, (unsigned)blocks(ks), 32 * kWarps, 0, s, g, ks);
+  auto run = [&](auto kern) { return launch_kernel(kern, (unsigned)blocks(ks), 32 * kWarps, 0, s, g, ks); };
+  if constexpr (sizeof(T) == 2 && !GATED)
+    if (g.a.planes == 2)
+      return vec ? run(dense_rows_kernel<T, GATED, MT, true, true>) : run(dense_rows_kernel<T, GATED, MT, false, true>);
+  return vec ? run(dense_rows_kernel<T, GATED, MT, true, false>) : run(dense_rows_kernel<T, GATED, MT, false, false>);
 }
 
 template <typename T, bool GATED>

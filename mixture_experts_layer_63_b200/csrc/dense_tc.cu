@@ -23,6 +23,7 @@
 // flight finish (bounded) and returns.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "dense_internal.h"
 #include "dense_math.cuh"
@@ -1057,7 +1058,17 @@ cudaError_t launch_dense_tc(const DenseGemm *g, int n, uint32_t *err, float *par
     return t;
   };
   const double pairs = std::max(1, device_sms() / 2);
-  auto cost = [&](int bn) { return std::max(1.0, (double)tiles_at(bn) / pairs) * (bn == 256 ? 1.0 : 0.8); };
+  // in steps of 256 columns: full waves, then a plain last wave or its cut form
+  auto cost = [&](int bn) {
+    double steps = 0;
+    for (int p = 0; p < n; ++p)
+      steps += (double)tiles_of(g[p], bn) * (double)((g[p].K + kBks * BK - 1) / (kBks * BK)) *
+               ((g[p].a2.p ? 2 : 1) * (g[p].dtype == MOE_F32 ? 6 : 1));
+    const double tiles = (double)tiles_at(bn), S = steps / tiles, full = std::floor(tiles / pairs);
+    const double rest = tiles - full * pairs;
+    const double last = rest == 0 ? 0 : std::min(S, rest * S / pairs + kJoinSteps + 2 * std::ceil(pairs / rest));
+    return (full * S + last) * (bn == 256 ? 1.0 : 0.8);
+  };
   P.bn = cost(128) < cost(256) ? 128 : 256;
   P.bnh = gated ? P.bn / 2 : P.bn;
   if (tiles_at(P.bn) > 0x3fffffff) return cudaErrorInvalidValue;
