@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
           T *o = static_cast<T *>(P.out) + (t0 + t + i * step) * P.ld_o + n;
           const float y = GATED ? v[i] * u[i] : v[i] + res[i];
           from_f32(*o, y);
-          if (P.lo_stride) from_f32(o[P.lo_stride], y - to_f32(*o));
+          if (P.lo_stride) from_f32(o[P.lo_stride], rest_of(y, to_f32(*o)));
         }
     }
   }

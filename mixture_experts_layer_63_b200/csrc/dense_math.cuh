@@ -13,6 +13,10 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ void from_f32(float &d, float v) { d = v; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16 &d, float v) { d = __float2bfloat16_rn(v); }
 
+// What rounding v to hi leaves for a low plane: nothing of what is no number or
+// rounds to an infinity, so that the planes' sum is hi and not inf - inf.
+__device__ __forceinline__ float rest_of(float v, float hi) { return fabsf(hi) <= 3.4028235e38f ? v - hi : 0.0f; }
+
 // 16 bytes of T from fp32 values, and back
 template <typename T>
 __device__ __forceinline__ uint4 pack16(const float *v) {
@@ -124,7 +128,8 @@ __device__ __forceinline__ void act_both(float v, float &f, float &d) {
   } else if (ACT == MOE_DENSE_GELU_TANH) {
     const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
     f = v * s;
-    d = s + v * s * (1.0f - s) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * v * v);
+    // (s (1 - s) is 0 long before the bound, which keeps 0 * inf out)
+    d = s + v * s * (1.0f - s) * (2.0f * kGeluA) * (1.0f + 3.0f * kGeluB * fminf(v * v, 1e8f));
   } else {
     f = v;
     d = 1.0f;

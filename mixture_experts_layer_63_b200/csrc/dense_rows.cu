@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(32 * kWarps) dense_rows_kernel(const DenseGemm
     }
     T *o = static_cast<T *>(P.out) + row * P.ld_o + n;
     from_f32(*o, a);
-    if (P.lo_stride) from_f32(o[P.lo_stride], a - to_f32(*o));
+    if (P.lo_stride) from_f32(o[P.lo_stride], rest_of(a, to_f32(*o)));
   }
 }
 

@@ -63,7 +63,7 @@ template <typename T>
 __device__ __forceinline__ void store_planes(void *base, int64_t at, int64_t lo_stride, float v) {
   T *p = static_cast<T *>(base) + at;
   from_f32(*p, v);
-  if (lo_stride) from_f32(p[lo_stride], v - to_f32(*p));
+  if (lo_stride) from_f32(p[lo_stride], rest_of(v, to_f32(*p)));
 }
 
 template <typename T>
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
             float h[V];
             unpack16<T>(hi, h);
 #pragma unroll
-            for (int j = 0; j < V; ++j) h[j] = v[j] - h[j];
+            for (int j = 0; j < V; ++j) h[j] = rest_of(v[j], h[j]);
             *reinterpret_cast<uint4 *>(dz + Q.lo_stride + (r + 8 * i) * Q.ld_dz + n) = pack16<T>(h);
           }
         }
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
           v *= d;
           T *o = dz + r * Q.ld_dz + c;
           from_f32(*o, v);
-          if (Q.lo_stride) from_f32(o[Q.lo_stride], v - to_f32(*o));
+          if (Q.lo_stride) from_f32(o[Q.lo_stride], rest_of(v, to_f32(*o)));
         }
         sum[j] += v;
       }

@@ -296,7 +296,7 @@ __device__ __forceinline__ uint4 low16(const float *v) {
   float h[E];
   unpack16<T>(pack16<T>(v), h);
 #pragma unroll
-  for (int i = 0; i < E; ++i) h[i] = v[i] - h[i];
+  for (int i = 0; i < E; ++i) h[i] = rest_of(v[i], h[i]);
   return pack16<T>(h);
 }
 // 16 bytes; the 256-byte stretch around them is brought to L2, where the

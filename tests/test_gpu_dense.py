@@ -174,6 +174,53 @@ def test_linear_infinite_and_nan_inputs_stay_in_their_rows(M, dtype):
     assert torch.equal(y[keep], y2[keep])
 
 
+@pytest.mark.parametrize("T", [1, 4, 16, 17, 130])
+def test_gated_overflow_is_an_infinity(T):
+    """A hidden value beyond bf16's range makes the results that read it
+    infinite, of the product's sign, however many rows the call has; the same
+    backward, for dA, dU and h.  (Powers of two: every product is exact, and the
+    other hidden values are too small to matter.)"""
+    K, f, inf = 16, 24, math.inf
+    x = torch.zeros(T, K, dtype=BF16, device="cuda")
+    x[:, 0] = 1.0
+    w1, w3 = (torch.zeros(f, K, dtype=BF16, device="cuda") for _ in range(2))
+    w1[:, 0], w3[:, 0] = 1.0, 1.0
+    w1[5, 0], w3[5, 0] = 2.0 ** 70, 2.0 ** 70
+    w2 = torch.ones(K, f, dtype=BF16, device="cuda")
+    w2[1::2, 5] = -1.0
+    y, dx = (torch.empty(T, K, dtype=BF16, device="cuda") for _ in range(2))
+    a, u = (torch.empty(T, f, dtype=BF16, device="cuda") for _ in range(2))
+    cfg = api.gated_ffn_config(T, K, f, "relu")
+    ws = api.new_gated_ffn_workspace(cfg, backward=True)
+    api.moe_gated_ffn(cfg, x, w1, None, w3, None, w2, None, None, y, a, u, ws)
+    assert (y[:, ::2] == inf).all() and (y[:, 1::2] == -inf).all()
+    # dh = 2^60 everywhere, u = 2^70 in column 5: dA, dU and h overflow there
+    dy = torch.zeros(T, K, dtype=BF16, device="cuda")
+    dy[:, 0] = 2.0 ** 60
+    dw1, dw3, db1 = torch.empty_like(w1), torch.empty_like(w1), torch.empty(f, dtype=BF16, device="cuda")
+    dw2, db3 = torch.empty_like(w2), torch.empty_like(db1)
+    api.moe_gated_ffn_backward(cfg, x, w1, w3, w2, a, u, dy, dx, dw1, db1, dw3, db3, dw2, None, ws)
+    api.moe_check_device_errors(ws)
+    for t in (dw1[5, 0], dw3[5, 0], dw2[0, 5], db1[5], db3[5]):
+        assert t == inf
+    assert (dx[:, 0] == inf).all()
+    assert dw1[4, 0] == T * 2.0 ** 60            # (T has at most 8 bits)
+
+
+def test_activation_gradients_far_out():
+    """act' of huge finite pre-activations is its limit, 0 or 1."""
+    v = torch.tensor([-3e38, -1e20, -1e4, 1e4, 1e20, 3e38], device="cuda")
+    for dtype in (BF16, F32):
+        for act in ("silu", "gelu", "gelu_tanh", "relu"):
+            for M in (1, 40):
+                z = v.to(dtype).repeat(M, 1)
+                cfg = api.linear_config(M, 8, 6, act, dtype)
+                db = torch.empty(6, dtype=dtype, device="cuda")
+                api.moe_linear_backward(cfg, None, None, z, torch.ones_like(z), None, None, db,
+                                        api.new_linear_workspace(cfg, backward=True))
+                assert db.tolist() == [0, 0, 0, M, M, M], (act, dtype, M)
+
+
 def test_linear_without_rows_launches_nothing():
     cfg = api.linear_config(0, 64, 64)
     ws = api.new_linear_workspace(cfg)
