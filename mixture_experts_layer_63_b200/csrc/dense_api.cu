@@ -79,6 +79,9 @@ moe_status dense_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_
 
 bool bad_ld(int64_t ld, int64_t width) { return ld != 0 && (ld < width || ld > kMaxRows); }
 
+// beyond any memory, and the byte counts here: 2^48 elements
+bool too_large(int64_t rows, int64_t ld) { return rows > 0 && ld > ((int64_t)1 << 48) / rows; }
+
 moe_status validate_act(int32_t act, int32_t dtype) {
   if (act < MOE_DENSE_IDENTITY || act > MOE_DENSE_GELU_TANH) return MOE_ERR_INVALID_ARG;
   return dtype == MOE_F32 || dtype == MOE_BF16 ? MOE_OK : MOE_ERR_INVALID_ARG;
@@ -93,20 +96,24 @@ moe_status validate_linear(const moe_linear_config *in, moe_linear_config *c) {
   if (st != MOE_OK) return st;
   if (bad_ld(c->ld_x, c->K) || bad_ld(c->ld_w, c->K) || bad_ld(c->ld_r, c->N) || bad_ld(c->ld_y, c->N))
     return MOE_ERR_INVALID_ARG;
-  if (c->M > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (c->ld_x == 0) c->ld_x = c->K;
   if (c->ld_w == 0) c->ld_w = c->K;
   if (c->ld_r == 0) c->ld_r = c->N;
   if (c->ld_y == 0) c->ld_y = c->N;
+  if (c->M > kMaxRows || too_large(c->M, std::max({c->ld_x, c->ld_r, c->ld_y})) || too_large(c->N, c->ld_w))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
-// Room for the tensor cores' copy of a [lines, inner] matrix whose lines are
-// ld elements apart: fp32 matrices (their planes) and bf16 ones with lines
-// that are not 16-byte aligned.
+// Do the tensor cores need a copy of a matrix with lines ld elements apart?
+// fp32: its planes; bf16: where a line is not 16-byte aligned.
+bool needs_copy(int dtype, int64_t lines, int64_t ld, const void *p = nullptr) {
+  return dtype == MOE_F32 || (lines > 1 && ld % 8 != 0) || reinterpret_cast<uintptr_t>(p) % 16 != 0;
+}
+size_t copy_room(int dtype, int64_t lines, int64_t inner) { return align256(pack_bytes(dtype, lines, inner)); }
+// Room for it, before the matrix's address is known
 size_t pack_room(int dtype, int64_t lines, int64_t inner, int64_t ld) {
-  if (dtype == MOE_BF16 && (lines <= 1 || ld % 8 == 0)) return 0;
-  return align256(pack_bytes(dtype, lines, inner));
+  return needs_copy(dtype, lines, ld) ? copy_room(dtype, lines, inner) : 0;
 }
 
 // bf16 calls of few rows hand dz, h, dA and dU from one product to the next in
@@ -132,12 +139,13 @@ struct LinearLayout {
 LinearLayout linear_layout(const moe_linear_config &c, bool backward) {
   LinearLayout L{};
   Taker t;
-  size_t room = pack_room(c.dtype, c.M, c.K, c.ld_x) + pack_room(c.dtype, c.N, c.K, c.ld_w);
+  // x and dy always have room for a copy: a column slice may start anywhere
+  size_t room = copy_room(c.dtype, c.M, c.K) + pack_room(c.dtype, c.N, c.K, c.ld_w);
   if (backward) {
     const bool act = c.act != MOE_DENSE_IDENTITY;
     L.dz = t.take(act ? (size_t)c.M * pack_ld(c.N) * dense_elem(c.dtype) * planes_of(c.dtype, c.M, true) : 0);
     L.part = t.take(colsum_scratch(c.M, c.N, 1));
-    room += pack_room(c.dtype, c.M, c.N, act ? pack_ld(c.N) : c.ld_y);
+    room += act ? pack_room(c.dtype, c.M, c.N, pack_ld(c.N)) : copy_room(c.dtype, c.M, c.N);
   }
   L.tail = t.take(tail_room(c.dtype, c.M, backward));
   L.pack = t.take(room);
@@ -166,6 +174,7 @@ class Products {
     }
     if (macs >= kTcMacs || depth > kSimtDepth || dtype_ == MOE_BF16) {
       DenseGemm q[4];
+      const size_t at = at_;
       bool ok = true;
       for (int i = 0; i < n && ok; ++i) {
         q[i] = g[i];
@@ -182,6 +191,7 @@ class Products {
         return launch_dense_tc(q, n, err, tail_ < first_ ? reinterpret_cast<float *>(base_ + tail_) : nullptr, s_);
       }
       jobs_ = launched_;
+      at_ = at;
     }
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < n && e == cudaSuccess; ++i) e = launch_dense_simt(g[i], s_);
@@ -203,13 +213,13 @@ class Products {
     if (!o->p || rows == 0 || K == 0) return true;
     const bool km = o->ks == 1;
     const int64_t lines = km ? rows : K, inner = km ? K : rows, ld = km ? o->rs : o->ks;
-    if (pack_room(dtype_, lines, inner, ld) == 0) return true;
+    if (!needs_copy(dtype_, lines, ld, o->p)) return true;
     int j = 0;
     while (j < jobs_ && !(job_[j].src == o->p && job_[j].lines == lines && job_[j].inner == inner &&
                           job_[j].ld == ld))
       ++j;
     if (j == jobs_) {
-      const size_t need = align256(pack_bytes(dtype_, lines, inner));
+      const size_t need = copy_room(dtype_, lines, inner);
       if (jobs_ == kMaxJobs || at_ + need > end_) return false;
       job_[jobs_++] = {o->p, lines, inner, ld, base_ + at_};
       at_ += need;
@@ -261,10 +271,12 @@ moe_status validate_gated(const moe_gated_ffn_config *in, moe_gated_ffn_config *
   if (st != MOE_OK) return st;
   if (bad_ld(c->ld_x, c->d_model) || bad_ld(c->ld_r, c->d_model) || bad_ld(c->ld_y, c->d_model))
     return MOE_ERR_INVALID_ARG;
-  if (c->T > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if (c->ld_x == 0) c->ld_x = c->d_model;
   if (c->ld_r == 0) c->ld_r = c->d_model;
   if (c->ld_y == 0) c->ld_y = c->d_model;
+  if (c->T > kMaxRows || too_large(c->T, std::max<int64_t>({c->ld_x, c->ld_r, c->ld_y, c->d_ff})) ||
+      too_large(c->d_ff, c->d_model))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -279,13 +291,14 @@ GatedLayout gated_layout(const moe_gated_ffn_config &c, bool backward) {
   const int64_t T = c.T, d = c.d_model, f = c.d_ff, ldh = pack_ld(f);
   const size_t tf = (size_t)T * ldh * dense_elem(c.dtype) * planes_of(c.dtype, T, backward);
   auto room = [&](int64_t lines, int64_t inner, int64_t ld) { return pack_room(c.dtype, lines, inner, ld); };
-  size_t pack = room(T, d, c.ld_x) + 2 * room(f, d, d) + room(d, f, f) + room(T, f, ldh);
+  size_t pack = copy_room(c.dtype, T, d) + 2 * room(f, d, d) + room(d, f, f) + room(T, f, ldh);
   L.h = t.take(tf);
   if (backward) {
     L.da = t.take(tf);
     L.du = t.take(tf);
-    L.part = t.take(colsum_scratch(T, std::max(c.d_ff, c.d_model), 3));
-    pack += 2 * room(T, f, ldh) + room(T, d, c.ld_y);
+    // (the sums of a subset may be cut into more parts than those of all)
+    L.part = t.take(std::max(colsum_scratch(T, c.d_ff, 3), colsum_scratch(T, c.d_model, 3)));
+    pack += 2 * room(T, f, ldh) + copy_room(c.dtype, T, d);
   }
   L.tail = t.take(tail_room(c.dtype, T, backward));
   L.pack = t.take(pack);

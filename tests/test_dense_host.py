@@ -63,6 +63,18 @@ def test_gated_configs(L, kw, status):
     assert size("moe_query_gated_ffn_size", gated(**kw))[0] == status
 
 
+def test_sizes_beyond_any_memory_are_refused(L):
+    """... before their byte counts pass 64 bits."""
+    big = 0x7fffffff
+    for c in (lin(M=big, N=big), lin(M=big, K=big), lin(K=big, N=big), lin(M=big, ld_x=big)):
+        assert size("moe_query_linear_size", c)[0] == UNSUPPORTED
+        assert size("moe_query_linear_size", c, 1)[0] == UNSUPPORTED
+    for c in (gated(T=big, d_ff=big), gated(d_model=big, d_ff=big), gated(T=big, d_model=big)):
+        assert size("moe_query_gated_ffn_size", c)[0] == UNSUPPORTED
+    st, n = size("moe_query_linear_size", lin(M=1 << 20, N=1 << 20))
+    assert st == OK and n < 1 << 40
+
+
 def linear_call(L, c, x=A(0), w=A(1), b=A(2), r=A(3), y=A(4), z=A(5), ws=A(6), nws=None):
     n = size("moe_query_linear_size", c)[1] if nws is None else nws
     return L.moe_linear(ctypes.byref(c), x, w, b, r, y, z, ws, n, None)

@@ -221,6 +221,38 @@ def test_activation_gradients_far_out():
                 assert db.tolist() == [0, 0, 0, M, M, M], (act, dtype, M)
 
 
+@pytest.mark.parametrize("off", [1, 4])
+@pytest.mark.parametrize("M", [40, 400])
+def test_column_slices_that_start_anywhere(M, off):
+    """x and dy as column slices of rows that are themselves aligned: the same
+    bits as from aligned copies (the same kernels run)."""
+    g = gen(21)
+    K, N = 264, 200
+    x, w, dy = (rnd(g, M, K, dtype=BF16, pad=8, off=off), rnd(g, N, K, dtype=BF16, std=0.06),
+                rnd(g, M, N, dtype=BF16, pad=8, off=off))
+    w1, w3, w2 = (rnd(g, *s, dtype=BF16, std=0.06) for s in ((N, K), (N, K), (K, N)))
+    gy = rnd(g, M, K, dtype=BF16, pad=8, off=off)
+    a, u = (rnd(g, M, N, dtype=BF16) for _ in range(2))
+    got = []
+    for copy in (False, True):
+        xs, ys, gs = (t.contiguous() if copy else t for t in (x, dy, gy))
+        cfg = api.linear_config(M, K, N, ld_x=xs.stride(0), ld_y=ys.stride(0))
+        wide = lambda n, t: torch.zeros(M, t.stride(0), dtype=BF16, device="cuda")[:, :n]  # noqa: E731
+        o = [wide(N, ys), wide(K, xs), torch.empty_like(w), wide(K, gs), wide(K, xs)]
+        o += [torch.empty_like(t) for t in (w1, w3, w2)]
+        ws = api.new_linear_workspace(cfg, backward=True)
+        api.moe_linear(cfg, xs, w, None, None, o[0], None, ws)
+        api.moe_linear_backward(cfg, xs, w, None, ys, o[1], o[2], None, ws)
+        gc = api.gated_ffn_config(M, K, N, ld_x=xs.stride(0), ld_y=gs.stride(0))
+        ws = api.new_gated_ffn_workspace(gc, backward=True)
+        api.moe_gated_ffn(gc, xs, w1, None, w3, None, w2, None, None, o[3], None, None, ws)
+        api.moe_gated_ffn_backward(gc, xs, w1, w3, w2, a, u, gs, o[4], o[5], None, o[6], None, o[7], None, ws)
+        api.moe_check_device_errors(ws)
+        got.append(o)
+    for p, q in zip(*got):
+        assert torch.equal(p, q)
+
+
 def test_linear_without_rows_launches_nothing():
     cfg = api.linear_config(0, 64, 64)
     ws = api.new_linear_workspace(cfg)
