@@ -8,6 +8,7 @@ without CUDA raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -784,18 +785,27 @@ def moe_clip_grads(grads, max_norm: float, norm, ws, out=None, stream=None):
                                                   q.stream(stream)))
 
 
+def _on_stream(stream):
+    """What a call allocates belongs to the stream it runs on: memory freed
+    there is reused there, behind the call."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
 class GatedFFN:
     """A dense gated feed-forward block between MoE layers: its weights and
     workspaces.  ``block(x, residual)`` runs moe_gated_ffn on any number of
     rows; with ``train=True`` it keeps the pre-activations for
-    ``block.backward(x, dy)``.  Workspaces grow with the largest batch seen;
-    calls of one object share them, so keep them on one stream."""
+    ``block.backward(x, dy)``.  Workspaces grow with the largest batch seen
+    (those that a captured graph uses stay for as long as the object); calls of
+    one object share them, so keep them, and replays, on one stream.  What a call
+    returns is allocated on the stream it runs on."""
 
     def __init__(self, w1, w3, w2, b1=None, b3=None, b2=None, act: str = "silu"):
         self.w1, self.w3, self.w2, self.b1, self.b3, self.b2, self.act = w1, w3, w2, b1, b3, b2, act
         self.ws = self.bws = None
         self.a = self.u = None
         self.cfgs: dict[tuple, MoeGatedFfnConfig] = {}
+        self.captured: list[torch.Tensor] = []      # what captured graphs read and write
 
     def _cfg(self, x, y, residual=None) -> MoeGatedFfnConfig:
         ld = [0 if t is None or t.shape[0] < 2 else t.stride(0) for t in (x, y, residual)]
@@ -809,9 +819,17 @@ class GatedFFN:
 
     def _room(self, ws, cfg, backward: bool):
         need = _query("moe_query_gated_ffn_size", ctypes.byref(cfg), int(backward))
-        return ws if ws is not None and ws.numel() >= need else _dense_workspace(need, self.w1.device)
+        if ws is None or ws.numel() < need:
+            ws = _dense_workspace(need, self.w1.device)
+        if torch.cuda.is_current_stream_capturing() and not any(ws is t for t in self.captured):
+            self.captured.append(ws)
+        return ws
 
     def __call__(self, x, residual=None, out=None, train: bool = False, stream=None):
+        with _on_stream(stream):
+            return self._forward(x, residual, out, train)
+
+    def _forward(self, x, residual, out, train: bool):
         y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         cfg = self._cfg(x, y, residual)
         self.ws = self._room(self.ws, cfg, False)
@@ -819,7 +837,7 @@ class GatedFFN:
             self.a = torch.empty(x.shape[0], self.w1.shape[0], dtype=x.dtype, device=x.device)
             self.u = torch.empty_like(self.a)
         moe_gated_ffn(cfg, x, self.w1, self.b1, self.w3, self.b3, self.w2, self.b2, residual, y,
-                      self.a if train else None, self.u if train else None, self.ws, stream)
+                      self.a if train else None, self.u if train else None, self.ws)
         return y
 
     def backward(self, x, dy, stream=None) -> dict:
@@ -828,6 +846,10 @@ class GatedFFN:
         dtype.  The residual's gradient is dy."""
         if self.a is None or self.a.shape[0] != x.shape[0]:
             raise ValueError("backward follows a forward with train=True on the same x")
+        with _on_stream(stream):
+            return self._backward(x, dy)
+
+    def _backward(self, x, dy) -> dict:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         g = {"dx": dx}
         for p in ("w1", "w3", "w2", "b1", "b3", "b2"):
@@ -839,7 +861,7 @@ class GatedFFN:
         cfg = self._cfg(xc, dy)
         self.bws = self._room(self.bws, cfg, True)
         moe_gated_ffn_backward(cfg, xc, self.w1, self.w3, self.w2, self.a, self.u, dy, dx, g["dw1"], g["db1"],
-                               g["dw3"], g["db3"], g["dw2"], g["db2"], self.bws, stream)
+                               g["dw3"], g["db3"], g["dw2"], g["db2"], self.bws)
         return g
 
 
@@ -852,6 +874,7 @@ def clip_grads(grads, max_norm: float, ws: torch.Tensor | None = None, stream=No
     for g in grads:
         flat += [t for k, t in g.items() if k != "dx"] if isinstance(g, dict) else [g]
     flat = [t for t in flat if t is not None]
-    norm = torch.empty((), dtype=torch.float32, device="cuda")
-    moe_clip_grads(flat, max_norm, norm, ws if ws is not None else new_clip_workspace(flat), stream=stream)
+    with _on_stream(stream):
+        norm = torch.empty((), dtype=torch.float32, device="cuda")
+        moe_clip_grads(flat, max_norm, norm, ws if ws is not None else new_clip_workspace(flat))
     return norm

@@ -601,6 +601,55 @@ def test_two_streams_with_their_own_workspaces():
     assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
 
 
+def test_block_and_clip_on_a_side_stream_own_what_they_use():
+    """Workspaces and outputs of a call on another stream are not handed out
+    again, on the current one, while the call still runs."""
+    g = gen(16)
+    T, K, f = 64, 256, 320
+    x, dy = rnd(g, T, K, dtype=BF16), rnd(g, T, K, dtype=BF16)
+    ws = [rnd(g, *s, dtype=BF16, std=0.06) for s in ((f, K), (f, K), (K, f))]
+    ref = api.GatedFFN(*ws)
+    y0 = ref(x, train=True)
+    g0 = ref.backward(x, dy)
+    grads = [t.clone() for t in (g0["dw1"], g0["dw2"])]
+    n0 = api.clip_grads([t.clone() for t in grads], 1e9)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)              # (about 10 ms)
+    block = api.GatedFFN(*ws)
+    y1 = block(x, train=True, stream=side)
+    g1 = block.backward(x, dy, stream=side)
+    n1 = api.clip_grads(grads, 1e9, stream=side)
+    small = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (512, 4096, 8192, 1 << 20) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y1) and n0 == n1 and all(torch.equal(g0[k], g1[k]) for k in ("dx", "dw1", "dw3", "dw2"))
+    assert all((t == 255).all() for t in small)
+
+
+def test_captured_block_outlives_larger_batches():
+    """A graph captured before the workspaces grew replays on the ones it was
+    captured with."""
+    g = gen(17)
+    K, f = 256, 320
+    block = api.GatedFFN(*(rnd(g, *s, dtype=BF16, std=0.06) for s in ((f, K), (f, K), (K, f))))
+    x, dy = rnd(g, 200, K, dtype=BF16), rnd(g, 200, K, dtype=BF16)
+    y0 = block(x, train=True)
+    g0 = block.backward(x, dy)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(x, train=True)
+        q = block.backward(x, dy)
+    big = rnd(g, 3000, K, dtype=BF16)
+    block(big, train=True)
+    block.backward(big, big)
+    junk = [torch.full((n << 20,), 255, dtype=torch.uint8, device="cuda") for n in (1, 2, 20, 42, 45, 60) for _ in range(2)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, y0) and all(torch.equal(q[k], g0[k]) for k in ("dx", "dw1", "dw3", "dw2"))
+    assert all((t == 255).all() for t in junk)
+
+
 def test_one_workspace_serves_different_calls_in_turn():
     """Cut tiles, copies and partial sums of one call leave nothing that the
     next call on the workspace reads."""
