@@ -40,6 +40,27 @@ __device__ __forceinline__ void unpack16(const uint4 &w, float *v) {
   }
 }
 
+// Two fp32 operations an instruction (sm_100a), each rounded as its scalar form
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+
 // 1 / (1 + e^-v).  FAST (bf16 layers, whose results are rounded to 8 bits
 // next): the reciprocal-based division and exponential, a few fp32 ulp.
 template <bool FAST>
@@ -71,6 +92,25 @@ __device__ __forceinline__ float normal_cdf_fast(float v, float &e) {
   q = fmaf(q, t, 0.14113952f);
   const float tail = q * t * e;
   return v > 0.0f ? 1.0f - tail : tail;
+}
+
+// The same of two values, most of it two operations an instruction (the
+// epilogues and the column sums are bound by instructions under GELU)
+__device__ __forceinline__ float2 normal_cdf_fast2(float2 v, float2 &e) {
+  const float2 x = make_float2(fabsf(v.x), fabsf(v.y));
+  const float2 g = mul2(mul2(two(-0.5f), v), v);
+  e = make_float2(__expf(g.x), __expf(g.y));
+  const float2 y = fma2(two(0.35355339f), x, two(1.0f));
+  const float2 t = make_float2(__fdividef(1.0f, y.x), __fdividef(1.0f, y.y));
+  float2 q = two(0.042448815f);
+  q = fma2(q, t, two(-0.17260440f));
+  q = fma2(q, t, two(0.18664083f));
+  q = fma2(q, t, two(0.024500929f));
+  q = fma2(q, t, two(0.13870965f));
+  q = fma2(q, t, two(0.13916363f));
+  q = fma2(q, t, two(0.14113952f));
+  const float2 tail = mul2(mul2(q, t), e), head = fma2(tail, two(-1.0f), two(1.0f));
+  return make_float2(v.x > 0.0f ? head.x : tail.x, v.y > 0.0f ? head.y : tail.y);
 }
 
 // Call f with the activation as a compile-time constant: one branch for a
@@ -124,7 +164,7 @@ __device__ __forceinline__ void act_both(float v, float &f, float &d) {
       c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
     }
     f = v * c;
-    d = c + v * (0.3989422804014327f * e);
+    d = fmaf(v, 0.3989422804014327f * e, c);
   } else if (ACT == MOE_DENSE_GELU_TANH) {
     const float s = sigmoid_t<FAST>(2.0f * kGeluA * (v + kGeluB * v * v * v));
     f = v * s;
@@ -133,6 +173,28 @@ __device__ __forceinline__ void act_both(float v, float &f, float &d) {
   } else {
     f = v;
     d = 1.0f;
+  }
+}
+
+// Two values at once, to the same bits
+template <bool FAST, int ACT>
+__device__ __forceinline__ float2 act_fwd2(float2 v) {
+  if (FAST && ACT == MOE_DENSE_GELU) {
+    float2 e;
+    return mul2(v, normal_cdf_fast2(v, e));
+  }
+  return make_float2(act_fwd<FAST, ACT>(v.x), act_fwd<FAST, ACT>(v.y));
+}
+template <bool FAST, int ACT>
+__device__ __forceinline__ void act_both2(float2 v, float2 &f, float2 &d) {
+  if (FAST && ACT == MOE_DENSE_GELU) {
+    float2 e;
+    const float2 c = normal_cdf_fast2(v, e);
+    f = mul2(v, c);
+    d = fma2(v, mul2(two(0.3989422804014327f), e), c);
+  } else {
+    act_both<FAST, ACT>(v.x, f.x, d.x);
+    act_both<FAST, ACT>(v.y, f.y, d.y);
   }
 }
 

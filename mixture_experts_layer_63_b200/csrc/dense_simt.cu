@@ -235,10 +235,11 @@ __global__ void __launch_bounds__(256, ACT == kNoAct ? 2 : 4) colsum_part_kernel
           float zz[V];
           unpack16<T>(b[i], zz);
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            float f, d;
-            act_both<sizeof(T) == 2, ACT>(zz[j], f, d);
-            v[j] *= d;
+          for (int j = 0; j < V; j += 2) {
+            float2 f, d;
+            act_both2<sizeof(T) == 2, ACT>(make_float2(zz[j], zz[j + 1]), f, d);
+            v[j] *= d.x;
+            v[j + 1] *= d.y;
           }
           uint4 *o = reinterpret_cast<uint4 *>(dz + (r + 8 * i) * Q.ld_dz + n);
           const uint4 hi = pack16<T>(v);

@@ -414,7 +414,11 @@ struct Epilogue {
         if (Q.pre) store_vals(packed(Q.pre), row0, col, v, stg, lane);
         with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < CW; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]);
+          for (int i = 0; i < CW; i += 2) {
+            const float2 y = act_fwd2<FAST, decltype(A)::value>(make_float2(v[i], v[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+          }
         });
         if (Q.residual) {
           in[0].stage(Rows<T>(Q.residual, Q.ld_r, Q.M, Q.N), row0, col, stg, lane);
@@ -444,7 +448,12 @@ struct Epilogue {
         }
         with_act(P.act, [&](auto A) {
 #pragma unroll
-          for (int i = 0; i < CW; ++i) v[i] = act_fwd<FAST, decltype(A)::value>(v[i]) * u[i];
+          for (int i = 0; i < CW; i += 2) {
+            const float2 f = act_fwd2<FAST, decltype(A)::value>(make_float2(v[i], v[i + 1]));
+            const float2 y = mul2(f, make_float2(u[i], u[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+          }
         });
         store_vals(out, row0, col, v, stg, lane);
       } else {                                           // kDenseGatedGrad
@@ -461,7 +470,7 @@ struct Epilogue {
           in[kIn - 1].stage(packed(Q.pre3_in), row0, col, stg_u, lane);
           __syncwarp();
           fetch(c + CW);
-          uint4 da[4], du[4], hh[4];
+          uint4 wa[4], wu[4], wh[4];
           with_act(P.act, [&](auto A) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -469,24 +478,28 @@ struct Epilogue {
               unpack16<T>(stg[stg_at(lane, k)], a);
               unpack16<T>(stg_u[stg_at(lane, k)], u);
 #pragma unroll
-              for (int i = 0; i < E; ++i) {
-                float f, d;
-                act_both<FAST, decltype(A)::value>(a[i], f, d);
-                const float dh = v[k * E + i];
-                a[i] = dh * u[i] * d;
-                h[i] = f * u[i];
-                u[i] = dh * f;
+              for (int i = 0; i < E; i += 2) {
+                float2 f, d;
+                act_both2<FAST, decltype(A)::value>(make_float2(a[i], a[i + 1]), f, d);
+                const float2 dh = make_float2(v[k * E + i], v[k * E + i + 1]), uu = make_float2(u[i], u[i + 1]);
+                const float2 da = mul2(mul2(dh, uu), d), hh = mul2(f, uu), du = mul2(dh, f);
+                a[i] = da.x;
+                a[i + 1] = da.y;
+                h[i] = hh.x;
+                h[i + 1] = hh.y;
+                u[i] = du.x;
+                u[i + 1] = du.y;
               }
-              da[k] = LOW ? low16<T>(a) : pack16<T>(a);
-              du[k] = LOW ? low16<T>(u) : pack16<T>(u);
-              hh[k] = LOW ? low16<T>(h) : pack16<T>(h);
+              wa[k] = LOW ? low16<T>(a) : pack16<T>(a);
+              wu[k] = LOW ? low16<T>(u) : pack16<T>(u);
+              wh[k] = LOW ? low16<T>(h) : pack16<T>(h);
             }
           });
           __syncwarp();
           const int64_t at = LOW ? Q.lo_stride : 0;
-          store_chunk(Rows<T>(static_cast<T *>(Q.out) + at, Q.ld_o, Q.M, Q.N), row0, col, da, stg, lane);
-          store_chunk(Rows<T>(static_cast<T *>(Q.out2) + at, Q.ld_o, Q.M, Q.N), row0, col, du, stg, lane);
-          store_chunk(Rows<T>(static_cast<T *>(Q.out3) + at, Q.ld_o, Q.M, Q.N), row0, col, hh, stg, lane);
+          store_chunk(Rows<T>(static_cast<T *>(Q.out) + at, Q.ld_o, Q.M, Q.N), row0, col, wa, stg, lane);
+          store_chunk(Rows<T>(static_cast<T *>(Q.out2) + at, Q.ld_o, Q.M, Q.N), row0, col, wu, stg, lane);
+          store_chunk(Rows<T>(static_cast<T *>(Q.out3) + at, Q.ld_o, Q.M, Q.N), row0, col, wh, stg, lane);
         };
         grads(IntC<0>{});
         if constexpr (EPI == kGradPlanes) grads(IntC<1>{});
