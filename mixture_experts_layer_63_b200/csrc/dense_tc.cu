@@ -357,10 +357,12 @@ __device__ __forceinline__ void add_bias(float (&v)[N], const float *bias) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     const float4 b = *reinterpret_cast<const float4 *>(bias + i);
-    v[i] += b.x;
-    v[i + 1] += b.y;
-    v[i + 2] += b.z;
-    v[i + 3] += b.w;
+    const float2 p = add2(make_float2(v[i], v[i + 1]), make_float2(b.x, b.y));
+    const float2 q = add2(make_float2(v[i + 2], v[i + 3]), make_float2(b.z, b.w));
+    v[i] = p.x;
+    v[i + 1] = p.y;
+    v[i + 2] = q.x;
+    v[i + 3] = q.y;
   }
 }
 
@@ -429,7 +431,11 @@ struct Epilogue {
             float r[E];
             unpack16<T>(stg[stg_at(lane, k)], r);
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[k * E + i] += r[i];
+            for (int i = 0; i < E; i += 2) {
+              const float2 y = add2(make_float2(v[k * E + i], v[k * E + i + 1]), make_float2(r[i], r[i + 1]));
+              v[k * E + i] = y.x;
+              v[k * E + i + 1] = y.y;
+            }
           }
           __syncwarp();
         }
