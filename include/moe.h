@@ -358,12 +358,15 @@ MOE_API moe_status moe_backward(const moe_config *cfg, const void *x, const void
  *   - tensors of rows take a row stride ld in elements (0: packed, the row
  *     width), and every pointer needs the alignment of its element type
  *     only.  Rows whose base address and stride are multiples of 16 bytes
- *     are read fastest;
+ *     are read fastest (others are copied first; bf16 weights with an aligned
+ *     stride and an unaligned base run on the CUDA cores, many times slower,
+ *     in calls of more than a few rows);
  *   - biases, residuals and gradients have the layer's dtype.  Sums are held
  *     in fp32 and each output is rounded once.  bf16: the intermediate
  *     matrices that a second product reads (h; in the backward passes dz, dA,
  *     dU and the remade h) are rounded to bf16 first (to 16 significant bits
- *     in calls of at most 16 rows, 4 backward);
+ *     in calls of at most 16 rows, 4 backward, where an infinite weight may
+ *     give NaN for an infinity);
  *   - fp32: products run in fp32, or on the tensor cores with each operand
  *     split exactly into three bf16 parts (an error of 2e-7 of the result's
  *     norm, below an fp32 product's own).  There an infinite element gives
