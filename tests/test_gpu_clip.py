@@ -183,3 +183,14 @@ def test_refusals():
         with pytest.raises(ValueError):
             api.moe_clip_grads(g, 1.0, norm, ws, out=out)
     assert (t == 1).all()
+
+
+def test_offsets_past_32_bits():
+    """Three elements behind the first 2^31 of a tensor, zeros before them."""
+    t = torch.zeros(2 ** 31 + 5, dtype=BF16, device="cuda")
+    t[-3:] = torch.tensor([3.0, 4.0, 12.0], dtype=BF16)
+    norm, ws = torch.empty((), device="cuda"), api.new_clip_workspace([t])
+    api.moe_clip_grads([t], 6.5, norm, ws)
+    assert norm.item() == 13.0
+    assert t[-3:].tolist() == [1.5, 2.0, 6.0]         # c = 0.5 (1 - 1e-7), rounded to bf16
+    assert not t[:-3].any()

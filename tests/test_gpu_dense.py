@@ -736,3 +736,65 @@ def test_results_repeat_bit_for_bit():
             got.append((y, dx, dw, db))
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+# ------------------------------- offsets past 32 bits ---------------------------------
+
+@pytest.mark.parametrize("dtype,M,K,N", [(BF16, 140000, 64, 16384), (BF16, 1, 16384, 140000), (BF16, 70, 16384, 140000),
+                                         (F32, 2, 16384, 140000)])
+def test_linear_offsets_past_32_bits(dtype, M, K, N):
+    """The last rows and columns of a result or a weight matrix of more than
+    2^31 elements, and its gradients."""
+    g = gen(30)
+    big = max(M * N, N * K)
+    assert big > 2 ** 31
+    x = rnd(g, M, K, dtype=dtype)
+    w = torch.empty(N, K, dtype=dtype, device="cuda")
+    w.normal_(std=K ** -0.5, generator=g)
+    y = torch.empty(M, N, dtype=dtype, device="cuda")
+    cfg = api.linear_config(M, K, N, "relu", dtype)
+    ws = api.new_linear_workspace(cfg)
+    api.moe_linear(cfg, x, w, None, None, y, None, ws)
+    api.moe_check_device_errors(ws)
+    del ws
+    rows, cols = slice(max(0, M - 40), M), slice(N - 300, N)
+    ref = x[rows].double() @ w[cols].double().T
+    e = ck(K) * (x[rows].double().abs() @ w[cols].double().abs().T)
+    ref = ref.clamp_min(0)
+    near(y[rows, cols], ref, e + U[dtype] * (ref + e), "y")
+    if M * N <= 2 ** 31:
+        return
+    ws = api.new_linear_workspace(cfg, backward=True)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(N, dtype=dtype, device="cuda")
+    z = y                                        # as pre-activations: the mask is y > 0
+    dy = torch.empty_like(y)
+    dy.normal_(generator=g)
+    api.moe_linear_backward(cfg, x, w, z, dy, dx, dw, db, ws)
+    api.moe_check_device_errors(ws)
+    dz = dy[rows].double() * (y[rows] > 0)
+    ref = dz @ w.double()
+    e = ck(N) * (dz.abs() @ w.double().abs())
+    near(dx[rows], ref, e + U[dtype] * (ref.abs() + e), "dx")
+    dzc = dy[:, cols].double() * (y[:, cols] > 0)
+    for got, ref, mag in ((dw[cols], dzc.T @ x.double(), dzc.abs().T @ x.double().abs()),
+                          (db[cols], dzc.sum(0), dzc.abs().sum(0))):
+        e = ck(M) * mag
+        near(got, ref, e + U[dtype] * (ref.abs() + e), "dw, db")
+
+
+def test_gated_offsets_past_32_bits():
+    g = gen(31)
+    T, K, f = 140000, 64, 16384
+    x = rnd(g, T, K, dtype=BF16)
+    w1, w3, w2 = (rnd(g, *s, dtype=BF16, std=s[1] ** -0.5) for s in ((f, K), (f, K), (K, f)))
+    y = torch.empty_like(x)
+    cfg = api.gated_ffn_config(T, K, f, "relu")
+    ws = api.new_gated_ffn_workspace(cfg)
+    api.moe_gated_ffn(cfg, x, w1, None, w3, None, w2, None, None, y, None, None, ws)
+    api.moe_check_device_errors(ws)
+    xs = x[-40:].double()
+    _, _, _, _, h, eh = gated_refs(xs, w1.double(), None, w3.double(), None, "relu", BF16)
+    eh = eh + U[BF16] * (h.abs() + eh)
+    ref = h @ w2.double().T
+    e = (eh + ck(f) * h.abs()) @ w2.double().abs().T
+    near(y[-40:], ref, e + U[BF16] * (ref.abs() + e), "y")
