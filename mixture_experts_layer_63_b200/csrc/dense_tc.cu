@@ -14,8 +14,8 @@
 // bias and GELU in 360 us alone (1.53 PFLOP/s, tensor pipe 88% busy), 1.27 in
 // the power-limited steady state; dx, dW1, dW3, dW2 of an 8192 x 2048 x 5632
 // block in one launch, 630 us (1.5 PFLOP/s).  At K = 2048 a tile's MMAs take
-// 16400 cycles and its epilogue 5700 (store), 9000 (residual), 12900 (GELU) or
-// 20300 and more (gradients), which then bounds it; fp32 4096^3: 650 us with its
+// 16400 cycles and its epilogue 5700 (store), 9000 (residual) or 20000 and more
+// (gradients), which then bounds it; fp32 4096^3: 650 us with its
 // splits (212 TFLOP/s).
 //
 //   warp 0     TMA producer             warp 2     TMEM allocation
