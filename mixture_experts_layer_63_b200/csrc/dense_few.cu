@@ -291,6 +291,41 @@ cudaError_t allow_smem() {
   return e;
 }
 
+// CTAs of `split` a cluster that are resident at once, per_sm of them an SM: the
+// GPCs hold whole clusters only.  One an SM: 132 CTAs in fours, 120 in eights (a
+// 16th cluster of eight ran alone: 31 us for 128 rows of 2048 x 5632, 20 in fours),
+// asked once a device.  Several an SM leave less over, about one SM in 64 a
+// step of the size (two an SM: 284 in fours, 264 in eights); the occupancy
+// query does not tell: it counts one CTA an SM for a kernel that allocates TMEM.
+int64_t resident(int split, int per_sm) {
+  if (per_sm > 1) return (int64_t)device_sms() * per_sm * (65 - split) / 64;
+  static std::atomic<int> cache[kMaxDevices][4];
+  int dev = 0, log = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  while (1 << log < split) ++log;
+  int n = dev < kMaxDevices ? cache[dev][log].load(std::memory_order_acquire) : 0;
+  if (n == 0) {
+    constexpr auto kern = dense_few_kernel<false, 1>;
+    if (allow_smem<kern>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kMaxSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)split, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = std::max(1, device_sms() / split);
+    }
+    n *= split;
+    if (dev < kMaxDevices) cache[dev][log].store(n, std::memory_order_release);
+  }
+  return n;
+}
+
 template <bool GATED, int U>
 cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, size_t smem, cudaStream_t s) {
   constexpr auto kern = dense_few_kernel<GATED, U>;
@@ -327,7 +362,7 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.tt = (int)std::min<int64_t>(128, (g.M + 15) / 16 * 16);
   P.planes = std::max(1, g.a.planes);
   const size_t stage = (size_t)nw * kWBytes + (size_t)P.planes * P.tt * BK * 2;
-  // CTAs an SM and CTAs a tile: what keeps most bytes in flight.  A CTA has at
+  // CTAs an SM and CTAs a tile: what keeps most bytes in flight at once.  A CTA has at
   // least two stages and six k-blocks; clusters of 1, 2, 4 or 8 (clusters of 3 fitted the SMs
   // badly: 88 us where 4 took 65, one row of a 5120 / 12288 gated block; 2 took
   // 75 us).
@@ -341,10 +376,10 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
     const int stages = (int)std::min<size_t>(kMaxStages, room / stage);
     if (stages < 2 || partial > room || per_sm * std::max(32, cols) > 512) continue;
     int split = 1;
-    while (split < 8 && tiles * ttiles * split * 2 <= (int64_t)device_sms() * per_sm && P.KB / (split * 2) >= 6)
+    while (split < 8 && tiles * ttiles * split * 2 <= resident(split * 2, per_sm) && P.KB / (split * 2) >= 6)
       split *= 2;
     // (one CTA an SM leaves the next kernel's no room to start beside it)
-    const double flight = (double)std::min<int64_t>(tiles * ttiles * split, (int64_t)device_sms() * per_sm) * stages *
+    const double flight = (double)std::min(tiles * ttiles * split, resident(split, per_sm)) * stages *
                           (per_sm == 1 ? 0.6 : 1.0);
     // (of two that keep as much, the fewer and deeper CTAs: 27 us against 45 for
     // 64 rows at 8192 x 4096, four stages and clusters of 4 against two and 8)
