@@ -363,7 +363,9 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.planes = std::max(1, g.a.planes);
   const size_t stage = (size_t)nw * kWBytes + (size_t)P.planes * P.tt * BK * 2;
   // CTAs an SM and CTAs a tile: what keeps most bytes in flight at once.  A CTA has at
-  // least two stages and six k-blocks; clusters of 1, 2, 4 or 8 (clusters of 3 fitted the SMs
+  // least two stages and six k-blocks, of many tokens (whose join costs more)
+  // twelve in a cluster of eight: 128 x 4096 x 5120 19 us in fours, 23 in eights, 48
+  // rows 15 in either.  Clusters of 1, 2, 4 or 8 (clusters of 3 fitted the SMs
   // badly: 88 us where 4 took 65, one row of a 5120 / 12288 gated block; 2 took
   // 75 us).
   P.KB = (int)((g.K + BK - 1) / BK);
@@ -376,7 +378,7 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
     const int stages = (int)std::min<size_t>(kMaxStages, room / stage);
     if (stages < 2 || partial > room || per_sm * std::max(32, cols) > 512) continue;
     int split = 1;
-    while (split < 8 && tiles * ttiles * split * 2 <= resident(split * 2, per_sm) && P.KB / (split * 2) >= 6)
+    while (split < 8 && tiles * ttiles * split * 2 <= resident(split * 2, per_sm) && P.KB / (split * 2) >= (split == 4 && P.tt > 64 ? 12 : 6))
       split *= 2;
     // (one CTA an SM leaves the next kernel's no room to start beside it)
     const double flight = (double)std::min(tiles * ttiles * split, resident(split, per_sm)) * stages *

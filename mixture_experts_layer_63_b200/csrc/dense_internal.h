@@ -80,9 +80,10 @@ inline size_t pack_bytes(int dtype, int64_t lines, int64_t inner) {
 cudaError_t launch_pack(int dtype, const PackJob *jobs, int n, cudaStream_t s);
 
 // Forward products of few rows (dense_few.cu): bf16, one tile of tokens.
-// Against 256-row tiles (dense_tc.cu), K = 4096, N = 14336: 27.5 us against 32.0
-// at 64 rows, 31.9 against 32.7 at 128, 48 against 34 at 192; N = 4096: 15.7
-// against 30 at 128; gated 80 against 129 (64), 88 against 128 (128).
+// Against 256-row tiles (dense_tc.cu), single calls from cold caches, K = 4096, N =
+// 14336: 37 us against 43 at 64 rows, 41 against 45 at 128, 57 against 45 at 192; N
+// = 4096: 20 against 31 at 128; the gated block 4096 / 14336 90 against 115 at 64
+// rows, 100 - 117 against 117 at 128, 147 against 117 at 192.
 constexpr int64_t kFewRows = 128;
 bool dense_few_ok(const DenseGemm &g);
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s);
