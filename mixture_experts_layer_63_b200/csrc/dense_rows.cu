@@ -152,10 +152,15 @@ cudaError_t rows_as(const DenseGemm &g, cudaStream_t s) {
   return vec ? run(dense_rows_kernel<T, GATED, MT, true, false>) : run(dense_rows_kernel<T, GATED, MT, false, false>);
 }
 
+// Rows of x a block.  bf16, whose lines are read element by element: up to three
+// rows one each, in blocks side by side that share the weights in L2 (two rows of
+// 4099 x 8192: 36 us, 52 with both in a block; three of 1411 x 2049: 7 against 13).
 template <typename T, bool GATED>
 cudaError_t rows_of(const DenseGemm &g, cudaStream_t s) {
-  return g.M == 1 ? rows_as<T, GATED, 1>(g, s) : g.M == 2 ? rows_as<T, GATED, 2>(g, s)
-         : g.M <= 4 ? rows_as<T, GATED, 4>(g, s) : rows_as<T, GATED, 8>(g, s);
+  if (g.M == 1 || (sizeof(T) == 2 && g.M <= 3)) return rows_as<T, GATED, 1>(g, s);
+  if constexpr (sizeof(T) == 4)
+    if (g.M == 2) return rows_as<T, GATED, 2>(g, s);
+  return g.M <= 4 ? rows_as<T, GATED, 4>(g, s) : rows_as<T, GATED, 8>(g, s);
 }
 
 }  // namespace
@@ -164,11 +169,14 @@ cudaError_t rows_of(const DenseGemm &g, cudaStream_t s) {
 // cores and their launch.  fp32, K = 4096, N = 8192: 28 us (1 row; 4.8 TB/s), 52
 // (8), 93 (16) against 145 whatever the rows, about 180 against 145 at 32; 1024 x
 // 1024: 9 against 31 at 32 rows.  bf16 with unaligned lines, K = 4099, N = 8192:
-// 17 against 47 us (1 row), 36 against 47 (2), 59 against 46 (4).
+// 23 against 46 us (1 row), 36 (2), 46 (3); 2051 x 4096: 16 against 17 at 3 rows, 21
+// at 4; gated 1411 / 5003: 49 against 41 at 3; 1027 x 1024: 8 against 10 at 8.
 bool dense_rows_ok(const DenseGemm &g) {
   if (g.epi != kDenseLinear && g.epi != kDenseGated) return false;
-  const bool small = g.K * g.N <= (int64_t)1 << 21;
-  return g.M <= (g.dtype == MOE_F32 ? (small ? 2 * kRegisterRows : kRegisterRows) : (small ? 8 : 2));
+  const int64_t size = g.K * g.N;
+  const bool small = size <= (int64_t)1 << 21;
+  if (g.dtype == MOE_F32) return g.M <= (small ? 2 * kRegisterRows : kRegisterRows);
+  return g.M <= (small ? 8 : size * (g.epi == kDenseGated ? 2 : 1) <= (int64_t)5 << 21 ? 3 : 2);
 }
 
 cudaError_t launch_dense_rows(const DenseGemm &g, cudaStream_t s) {
