@@ -176,7 +176,7 @@ bool dense_rows_ok(const DenseGemm &g) {
   const int64_t size = g.K * g.N;
   const bool small = size <= (int64_t)1 << 21;
   if (g.dtype == MOE_F32) return g.M <= (small ? 2 * kRegisterRows : kRegisterRows);
-  return g.M <= (small ? 8 : size * (g.epi == kDenseGated ? 2 : 1) <= (int64_t)5 << 21 ? 3 : 2);
+  return g.M <= (small ? 8 : size * (g.epi == kDenseGated || g.a.planes == 2 ? 2 : 1) <= (int64_t)5 << 21 ? 3 : 2);
 }
 
 cudaError_t launch_dense_rows(const DenseGemm &g, cudaStream_t s) {
