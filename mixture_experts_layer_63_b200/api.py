@@ -676,6 +676,7 @@ def _query(fn: str, *args) -> int:
 
 
 def _dense_workspace(nbytes: int, device) -> torch.Tensor:
+    """(Made during a capture, its control block is cleared by the replay only.)"""
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     ws[:4096].zero_()                       # the control block
     return ws
@@ -795,14 +796,18 @@ class GatedFFN:
     """A dense gated feed-forward block between MoE layers: its weights and
     workspaces.  ``block(x, residual)`` runs moe_gated_ffn on any number of
     rows; with ``train=True`` it keeps the pre-activations for
-    ``block.backward(x, dy)``.  Workspaces grow with the largest batch seen
-    (those that a captured graph uses stay for as long as the object); calls of
-    one object share them, so keep them, and replays, on one stream.  What a call
-    returns is allocated on the stream it runs on."""
+    ``block.backward(x, dy)``.  Workspaces grow with the largest batch seen;
+    calls of one object share them, so keep them, and replays, on one stream.
+    What a captured graph uses (workspaces, and the pre-activations that a
+    captured backward reads) stays for as long as the object; a workspace that
+    has to be made during a capture serves captured calls only, each of which
+    clears its control block.  What a call returns is allocated on the stream it
+    runs on."""
 
     def __init__(self, w1, w3, w2, b1=None, b3=None, b2=None, act: str = "silu"):
         self.w1, self.w3, self.w2, self.b1, self.b3, self.b2, self.act = w1, w3, w2, b1, b3, b2, act
         self.ws = self.bws = None
+        self.graph_ws: dict[bool, torch.Tensor] = {}    # made during captures (True: backward)
         self.a = self.u = None
         self.cfgs: dict[tuple, MoeGatedFfnConfig] = {}
         self.captured: list[torch.Tensor] = []      # what captured graphs read and write
@@ -817,13 +822,33 @@ class GatedFFN:
                 self.cfgs[key] = c
         return c
 
-    def _room(self, ws, cfg, backward: bool):
+    def _room(self, cfg, backward: bool):
         need = _query("moe_query_gated_ffn_size", ctypes.byref(cfg), int(backward))
-        if ws is None or ws.numel() < need:
-            ws = _dense_workspace(need, self.w1.device)
-        if torch.cuda.is_current_stream_capturing() and not any(ws is t for t in self.captured):
-            self.captured.append(ws)
+        ws = self.bws if backward else self.ws
+        if ws is not None and ws.numel() >= need:
+            self._keep(ws)
+            return ws
+        if torch.cuda.is_current_stream_capturing():
+            # What is recorded here runs at the replay, the clearing of the
+            # control block too: nothing else may take this workspace for a
+            # cleared one, and every graph that uses it clears it.
+            ws = self.graph_ws.get(backward)
+            if ws is None or ws.numel() < need:
+                ws = self.graph_ws[backward] = torch.empty(need, dtype=torch.uint8, device=self.w1.device)
+            ws[:4096].zero_()
+            self._keep(ws)
+            return ws
+        ws = _dense_workspace(need, self.w1.device)
+        if backward:
+            self.bws = ws
+        else:
+            self.ws = ws
         return ws
+
+    def _keep(self, *tensors):
+        """What a capture that is under way reads or writes lives as long as the object."""
+        if torch.cuda.is_current_stream_capturing():
+            self.captured += [t for t in tensors if not any(t is k for k in self.captured)]
 
     def __call__(self, x, residual=None, out=None, train: bool = False, stream=None):
         with _on_stream(stream):
@@ -832,12 +857,12 @@ class GatedFFN:
     def _forward(self, x, residual, out, train: bool):
         y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
         cfg = self._cfg(x, y, residual)
-        self.ws = self._room(self.ws, cfg, False)
+        ws = self._room(cfg, False)
         if train:
             self.a = torch.empty(x.shape[0], self.w1.shape[0], dtype=x.dtype, device=x.device)
             self.u = torch.empty_like(self.a)
         moe_gated_ffn(cfg, x, self.w1, self.b1, self.w3, self.b3, self.w2, self.b2, residual, y,
-                      self.a if train else None, self.u if train else None, self.ws)
+                      self.a if train else None, self.u if train else None, ws)
         return y
 
     def backward(self, x, dy, stream=None) -> dict:
@@ -859,9 +884,10 @@ class GatedFFN:
         # dx is packed here: the strided x of the configuration would also be dx's
         xc = x if T < 2 or x.stride(0) == x.shape[1] else x.contiguous()
         cfg = self._cfg(xc, dy)
-        self.bws = self._room(self.bws, cfg, True)
+        ws = self._room(cfg, True)
+        self._keep(self.a, self.u)
         moe_gated_ffn_backward(cfg, xc, self.w1, self.w3, self.w2, self.a, self.u, dy, dx, g["dw1"], g["db1"],
-                               g["dw3"], g["db3"], g["dw2"], g["db2"], self.bws)
+                               g["dw3"], g["db3"], g["dw2"], g["db2"], ws)
         return g
 
 
