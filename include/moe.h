@@ -480,10 +480,10 @@ MOE_API moe_status moe_grad_norm(const moe_grad *grads, int32_t count, float *no
 
 /* The same norm, then dst = c * src with c = min(1, max_norm / (norm + 1e-6))
  * in fp32 (one rounding to the tensor's dtype).  max_norm > 0 (infinity: c =
- * 1 whatever the norm).  No host sync: c is computed on the device.  An
- * infinite element makes the norm infinite and c = 0 (then inf * 0 = NaN in
- * that place), a NaN makes every result NaN; norm shows it.  norm may be
- * NULL.  No two of the tensors written may overlap, nor one written and
+ * 1 whatever the norm).  No host sync: c is computed on the device.  Under a
+ * finite max_norm an infinite element makes the norm infinite and c = 0 (then
+ * inf * 0 = NaN in that place), a NaN makes every result NaN; norm shows it.
+ * norm may be NULL.  No two of the tensors written may overlap, nor one written and
  * another read (a tensor listed twice: MOE_ERR_INVALID_ARG). */
 MOE_API moe_status moe_clip_grads(const moe_grad *grads, int32_t count, float max_norm, float *norm, void *ws,
                                   size_t ws_bytes, moe_stream_t stream);

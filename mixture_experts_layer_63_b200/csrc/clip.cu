@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
   if (max_norm < 0.0f) return;
   const double ratio = (double)max_norm / (n + kClipEps);
-  const float c = ratio > 1.0 ? 1.0f : (float)ratio;        // a NaN norm gives a NaN factor
+  // a NaN norm gives a NaN factor; no limit, no factor, whatever the norm
+  const float c = ratio > 1.0 || isinf(max_norm) ? 1.0f : (float)ratio;
   // last chunks first: the norm's pass read them last, so they may still be in L2
   for (int k = t.first[t.count] - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
     const int i = tensor_of(t, k);
