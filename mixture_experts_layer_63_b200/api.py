@@ -735,9 +735,10 @@ def moe_gated_ffn_backward(cfg, x, w1, w3, w2, a, u, dy, dx, dw1, db1, dw3, db3,
 
 
 def _grad_list(grads, out=None):
-    """The C list of a sequence of contiguous CUDA tensors (None entries are
-    skipped): the bytes of moe_grad entries, and their number."""
+    """The C list of some contiguous CUDA tensors (None entries are skipped):
+    the bytes of moe_grad entries, and their number."""
     dev, vals, n = None, [], 0
+    grads = list(grads)                     # (an iterator would be read twice side by side)
     for g, o in zip(grads, out if out is not None else grads, strict=True):
         if g is None:
             continue
@@ -752,6 +753,8 @@ def _grad_list(grads, out=None):
         src, size = g.data_ptr(), g.numel()
         dst = src
         if o is not g:
+            if o is None:
+                raise ValueError("a gradient without an output")
             if o.get_device() != dev:
                 _on_device(o)
             if not o.is_contiguous() or o.dtype != g.dtype or o.numel() != size:
@@ -763,7 +766,7 @@ def _grad_list(grads, out=None):
 
 
 def new_clip_workspace(grads, device="cuda") -> torch.Tensor:
-    """A workspace for moe_grad_norm / moe_clip_grads on a list of this length."""
+    """A workspace for moe_grad_norm / moe_clip_grads on a list (or any collection) of this length."""
     return _dense_workspace(_query("moe_query_clip_size", len(grads)), device)
 
 
