@@ -413,7 +413,8 @@ MOE_API moe_status moe_linear(const moe_linear_config *cfg, const void *x, const
  * (The residual's gradient is dy itself.)  z: as moe_linear wrote it; not
  * read, and may be NULL, with MOE_DENSE_IDENTITY.  dx [M, K], dw [N, K]
  * (packed), dbias [N] are overwritten; each may be NULL (not computed), not
- * all three.  relu'(0) = 0.  M = 0 gives zero dw and dbias. */
+ * all three.  relu'(0) = 0, act'(NaN) = NaN.
+ * M = 0 gives zero dw and dbias. */
 MOE_API moe_status moe_linear_backward(const moe_linear_config *cfg, const void *x, const void *w,
                                        const void *z, const void *dy, void *dx, void *dw, void *dbias,
                                        void *ws, size_t ws_bytes, moe_stream_t stream);

@@ -182,12 +182,13 @@ __device__ __forceinline__ float act_fwd(float v) {
   return v;
 }
 
-// act(v) and act'(v); relu'(0) = 0, as in the MoE layer's backward pass
+// act(v) and act'(v); relu'(0) = 0, as in the MoE layer's backward pass, and a
+// NaN stays a NaN in both
 template <bool FAST, int ACT>
 __device__ __forceinline__ void act_both(float v, float &f, float &d) {
   if (ACT == MOE_DENSE_RELU) {
     f = v < 0.0f ? 0.0f : v;
-    d = v > 0.0f ? 1.0f : 0.0f;
+    d = v > 0.0f ? 1.0f : v <= 0.0f ? 0.0f : v;
   } else if (ACT == MOE_DENSE_SILU) {
     const float s = gate_of<FAST, ACT>(v);
     f = v * s;
