@@ -365,13 +365,13 @@ MOE_API moe_status moe_backward(const moe_config *cfg, const void *x, const void
  *     in fp32 and each output is rounded once.  bf16: the intermediate
  *     matrices that a second product reads (h; in the backward passes dz, dA,
  *     dU and the remade h) are rounded to bf16 first (to 16 significant bits
- *     in calls of at most 16 rows, 4 backward, where an infinite weight may
- *     give NaN for an infinity);
+ *     in calls of at most 16 rows, 4 backward; in the latter an infinite
+ *     weight or input may give NaN for an infinity);
  *   - fp32: products run in fp32, or on the tensor cores with each operand
  *     split exactly into three bf16 parts (an error of 2e-7 of the result's
- *     norm, below an fp32 product's own).  There an infinite element gives
- *     NaN where fp32 arithmetic would give an infinity, and elements below
- *     2^-108 lose low bits;
+ *     norm, below an fp32 product's own).  Infinite and NaN elements act as in
+ *     fp32 arithmetic.  Elements below 2^-108 lose low bits, and where the
+ *     product of two elements passes 2^127, NaN may stand for an infinity;
  *   - a workspace serves one call at a time, of any of these entry points that
  *     it is large enough for; its 4 KiB control block must have been cleared
  *     once (moe_workspace_init);

@@ -191,8 +191,13 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
         uint32_t lo[16];
         tmem_ld16(ta + P.tt + c, lo);
         tmem_ld_wait();
+        // (an infinite weight makes the high plane's sum infinite; times a low
+        // part, which may be 0 or of the other sign, it would say NaN)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(lo[i]));
+        for (int i = 0; i < 16; ++i) {
+          const float hi = __uint_as_float(r[i]);
+          if (isfinite(hi)) r[i] = __float_as_uint(hi + __uint_as_float(lo[i]));
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) part[(c + i) * BN + row] = kb1 > kb0 ? __uint_as_float(r[i]) : 0.0f;

@@ -1,4 +1,4 @@
-"""NaN in the dense operators: which results it reaches is compared with the
+"""NaN and infinities in the dense operators: which results it reaches is compared with the
 formulas' in 64 bits, place by place, and every other result with what the call
 gives without it, bit for bit."""
 import math
@@ -87,3 +87,74 @@ def test_nan_pre_activation_of_a_gated_backward(where, T, act, dtype):
     for n in ref:
         check(got[n], clean[n], ref[n], n)
     assert got["dw2"][:, 101].isnan().all()
+
+
+def spots(t, places, values):
+    t = t.clone()
+    for (i, j), v in zip(places, values):
+        t[i, j] = v
+    return t
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M", [1, 3, 12, 20, 40, 150, 300])
+@pytest.mark.parametrize("side", ["x", "w", "both"])
+def test_infinite_elements_of_a_linear_forward(side, M, dtype):
+    """inf v = +-inf, inf 0 = NaN, inf - inf = NaN, inf inf = inf, whatever the
+    rows: sizes on every kernel."""
+    g = gen(62)
+    for K, N in ((136, 200), (4096, 264)):
+        x, w = rnd(g, M, K, dtype=dtype), rnd(g, N, K, dtype=dtype, std=0.1)
+        w[3, 5] = 0.0
+        clean, got = (torch.empty(M, N, dtype=dtype, device="cuda") for _ in range(2))
+        cfg = api.linear_config(M, K, N, "identity", dtype)
+        ws = api.new_linear_workspace(cfg)
+        api.moe_linear(cfg, x, w, None, None, clean, None, ws)
+        if side != "w":
+            x = spots(x, [(M - 1, 5), (M // 2, 7), (M // 2, 100)], [math.inf, -math.inf, math.inf])
+        if side != "x":
+            w = spots(w, [(9, 5), (9, 131), (N - 1, 7)], [math.inf, math.inf, -math.inf])
+        api.moe_linear(cfg, x, w, None, None, got, None, ws)
+        api.moe_check_device_errors(ws)
+        check(got, clean, x.double() @ w.double().T, f"{K} x {N}")
+
+
+@pytest.mark.parametrize("M", [6, 40, 300])
+def test_infinite_elements_of_an_fp32_linear_backward(M):
+    g = gen(63)
+    K, N = 264, 392
+    x, w, dy = rnd(g, M, K, dtype=F32), rnd(g, N, K, dtype=F32, std=0.1), rnd(g, M, N, dtype=F32)
+    cfg = api.linear_config(M, K, N, "identity", F32)
+    ws = api.new_linear_workspace(cfg, backward=True)
+
+    def run():
+        o = [torch.empty_like(x), torch.empty_like(w), torch.empty(N, device="cuda")]
+        api.moe_linear_backward(cfg, x, w, None, dy, *o, ws)
+        return o
+    clean = run()
+    x, w = spots(x, [(1, 200)], [-math.inf]), spots(w, [(300, 17), (301, 17)], [math.inf, -math.inf])
+    dy = spots(dy, [(M - 1, 2), (1, 3)], [math.inf, -math.inf])
+    got = run()
+    api.moe_check_device_errors(ws)
+    for p, q, r, n in zip(got, clean, (dy.double() @ w.double(), dy.double().T @ x.double(), dy.double().sum(0)),
+                          ("dx", "dw", "db")):
+        check(p, q, r, n)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 7, 16, 17, 130, 300])
+def test_infinite_weights_of_a_gated_block(T, dtype):
+    """The second product's: h is handed on in planes, of few rows too."""
+    g = gen(64)
+    K, f = 136, 328
+    x = rnd(g, T, K, dtype=dtype)
+    w1, w3, w2 = (rnd(g, *s, dtype=dtype, std=0.1) for s in ((f, K), (f, K), (K, f)))
+    clean, got = (torch.empty(T, K, dtype=dtype, device="cuda") for _ in range(2))
+    cfg = api.gated_ffn_config(T, K, f, "silu", dtype)
+    ws = api.new_gated_ffn_workspace(cfg)
+    api.moe_gated_ffn(cfg, x, w1, None, w3, None, w2, None, None, clean, None, None, ws)
+    w2 = spots(w2, [(5, 300), (60, 0), (60, 9)], [math.inf, -math.inf, -math.inf])
+    api.moe_gated_ffn(cfg, x, w1, None, w3, None, w2, None, None, got, None, None, ws)
+    api.moe_check_device_errors(ws)
+    h = act64(x.double() @ w1.double().T, "silu") * (x.double() @ w3.double().T)
+    check(got, clean, h @ w2.double().T, "y")
