@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "dense_few_plan.h"
 #include "dense_internal.h"
 #include "dense_math.cuh"
 #include "sm100_ptx.cuh"
@@ -24,11 +25,10 @@
 namespace moe {
 namespace {
 
-constexpr int BN = 128;                 // rows of W a CTA (the MMA's M)
-constexpr int BK = 64;
+constexpr int BN = kFewBN, BK = kFewBK;
 constexpr int kThreads = 256;
-constexpr int kMaxStages = 8;
-constexpr uint32_t kWBytes = BN * BK * 2;
+constexpr int kMaxStages = kFewMaxStages;
+constexpr uint32_t kWBytes = kFewWBytes;
 
 struct FewParams {
   CUtensorMap x, w, w3;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
 }
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kMaxSmem = 220 * 1024;
+constexpr size_t kMaxSmem = kFewMaxSmem;
 
 template <auto kern>
 cudaError_t allow_smem() {
@@ -362,43 +362,14 @@ bool dense_few_ok(const DenseGemm &g) {
 
 cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) {
   const bool gated = g.epi == kDenseGated;
-  const int nw = gated ? 2 : 1;
   FewParams P{};
-  P.tt = (int)std::min<int64_t>(128, (g.M + 15) / 16 * 16);
   P.planes = std::max(1, g.a.planes);
-  const size_t stage = (size_t)nw * kWBytes + (size_t)P.planes * P.tt * BK * 2;
-  // CTAs an SM and CTAs a tile: what keeps most bytes in flight at once.  A CTA has at
-  // least two stages and six k-blocks, of many tokens (whose join costs more)
-  // twelve in a cluster of eight: 128 x 4096 x 5120 19 us in fours, 23 in eights, 48
-  // rows 15 in either.  Clusters of 1, 2, 4 or 8 (clusters of 3 fitted the SMs
-  // badly: 88 us where 4 took 65, one row of a 5120 / 12288 gated block; 2 took
-  // 75 us).
-  P.KB = (int)((g.K + BK - 1) / BK);
-  const int64_t tiles = (g.N + BN - 1) / BN, ttiles = (g.M + P.tt - 1) / P.tt;
-  const size_t partial = (size_t)nw * P.tt * BN * 4;
-  const int cols = P.planes * nw * P.tt;                     // of the accumulators
-  double best = 0;
-  for (int per_sm = 1; per_sm <= 4; ++per_sm) {
-    const size_t room = kMaxSmem / per_sm - (per_sm > 1 ? 2048 : 1024);       // stages or partial tile of a CTA
-    const int stages = (int)std::min<size_t>(kMaxStages, room / stage);
-    if (stages < 2 || partial > room || per_sm * std::max(32, cols) > 512) continue;
-    int split = 1;
-    while (split < 8 && tiles * ttiles * split * 2 <= resident(split * 2, per_sm) && P.KB / (split * 2) >= (split == 4 && P.tt > 64 ? 12 : 6))
-      split *= 2;
-    // (one CTA an SM leaves the next kernel's no room to start beside it)
-    const double flight = (double)std::min(tiles * ttiles * split, resident(split, per_sm)) * stages *
-                          (per_sm == 1 ? 0.6 : 1.0);
-    // (of two that keep as much, the fewer and deeper CTAs: 27 us against 45 for
-    // 64 rows at 8192 x 4096, four stages and clusters of 4 against two and 8)
-    if (flight > best) {
-      best = flight;
-      P.stages = stages;
-      P.split = split;
-    }
-  }
-  P.tmem_cols = 32;
-  while (P.tmem_cols < cols) P.tmem_cols *= 2;
-  const size_t smem = 1024 + std::max(P.stages * stage, (size_t)nw * P.tt * BN * 4);
+  const FewPlan plan = few_plan(g.M, g.K, g.N, gated, P.planes, resident);
+  P.tt = plan.tt;
+  P.KB = plan.KB;
+  P.stages = plan.stages;
+  P.split = plan.split;
+  P.tmem_cols = plan.tmem_cols;
   auto map = [&](CUtensorMap *m, const Operand &o, int64_t rows, int box) {
     const int64_t ld = rows == 1 ? pack_ld(g.K) : o.rs;
     return make_map3d(m, o.p, g.K, rows, std::max(1, o.planes), ld, o.planes > 1 ? o.plane_stride : ld * rows, box,
@@ -421,7 +392,8 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.err = err;
   // a thread's tokens at a time: all of them, up to four (eight with one
   // matrix), so that their loads are in flight together; more would be idle loads
-  const unsigned nt = (unsigned)tiles, tt = (unsigned)ttiles;
+  const unsigned nt = (unsigned)plan.tiles, tt = 1;
+  const size_t smem = plan.smem;
   const int64_t each = (g.M + 2 * P.split - 1) / (2 * P.split);
   if (each <= 1) return gated ? launch_few_as<true, 1>(P, nt, tt, smem, s) : launch_few_as<false, 1>(P, nt, tt, smem, s);
   if (each <= 2) return gated ? launch_few_as<true, 2>(P, nt, tt, smem, s) : launch_few_as<false, 2>(P, nt, tt, smem, s);

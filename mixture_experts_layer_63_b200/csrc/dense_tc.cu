@@ -34,6 +34,7 @@
 #include "dense_internal.h"
 #include "dense_math.cuh"
 #include "sm100_ptx.cuh"
+#include "tmem_share.h"
 
 namespace moe {
 namespace {
@@ -958,6 +959,7 @@ cudaError_t launch_pair_as(TcParams &P, cudaStream_t s) {
   constexpr auto kern = dense_pair_kernel<EPI, T>;
   constexpr size_t smem = 1024 + kStages * kBks * (kABytes + 128 * BK * 2) +
                           kEpiWarps * Epilogue<EPI, T>::kIn * kStgBytes;
+  static_assert(smem >= kAllTmemSmem, "beside kernels that allocate fewer columns");
   int pairs = 0;
   const cudaError_t e = pairs_of<kern>(smem, &pairs);
   if (e != cudaSuccess) return e;

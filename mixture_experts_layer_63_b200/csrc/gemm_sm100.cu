@@ -40,6 +40,7 @@
 #include "device_common.cuh"
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
+#include "tmem_share.h"
 
 namespace moe {
 namespace {
@@ -2151,8 +2152,9 @@ cudaError_t launch_grouped_gemm(const GroupedGemm &g, cudaStream_t s) {
     const bool bk2 = bk2_tn;
     const size_t stage = (size_t)(bk2 ? 2 : 1) * ((size_t)kABytes + (size_t)(maxn / 2) * BK * 2);
     const size_t nstages = bk2 ? (size_t)kPairStages2 : (size_t)kPairStages;
-    const size_t tsmem = nstages * stage + 1024 + 4 * (size_t)kTnStgBytes +
-                         (swiglu ? (size_t)kTnXchBytes : 0);
+    const size_t tsmem = tmem_smem(nstages * stage + 1024 + 4 * (size_t)kTnStgBytes +
+                                       (swiglu ? (size_t)kTnXchBytes : 0),
+                                   kTmemCols);
 #define MOE_TN_CASE(E_)                                                                  \
   case E_:                                                                               \
     return bk2 ? launch_tn<E_, 2>(Q, maps, max_tiles, tsmem, s)                          \
@@ -2222,10 +2224,10 @@ cudaError_t launch_grouped_gemm(const GroupedGemm &g, cudaStream_t s) {
   // (with stream-K, every SM: a short problem's k-blocks are spread over all)
   const int grid = std::min(kSkSlots, (int)std::max<int64_t>(1, std::min<int64_t>(
                                           device_sms(), sk ? device_sms() : max_tiles)));
-  // at least 120 KB so that one CTA (and one 512-column TMEM allocation) fits per SM
-  const size_t smem = std::max<size_t>((size_t)kStages * (kABytes + (size_t)P.bn * BK * 2) + 1024 +
-                                           4 * kStageBytesPerWarp,
-                                       (size_t)120 * 1024);
+  // (so that one CTA, and one allocation of all TMEM columns, fits per SM)
+  const size_t smem = tmem_smem((size_t)kStages * (kABytes + (size_t)P.bn * BK * 2) + 1024 +
+                                    4 * kStageBytesPerWarp,
+                                kTmemCols);
 
   if (pair) {
     const int64_t pt_routed = (g.max_routed_rows + 2 * BM - 1) / (2 * BM) + g.n_routed;
@@ -2240,9 +2242,10 @@ cudaError_t launch_grouped_gemm(const GroupedGemm &g, cudaStream_t s) {
                         g.K * (swiglu_b(g.epi) ? 2 : 1);
     const bool bk2 = MOE_PAIR_BK128 && !g.kgroup && !g.b_mn && !g.gather_rows &&
                      g.K % (2 * BK) == 0 && macs >= 2e11;
-    const size_t psmem = (bk2 ? (size_t)kPairStages2 * 2 : (size_t)kPairStages) *
-                             (kABytes + (size_t)(P.bn / 2) * BK * 2) +
-                         1024 + 4 * kStageBytesPerWarp;
+    const size_t psmem = tmem_smem((bk2 ? (size_t)kPairStages2 * 2 : (size_t)kPairStages) *
+                                           (kABytes + (size_t)(P.bn / 2) * BK * 2) +
+                                       1024 + 4 * kStageBytesPerWarp,
+                                   kTmemCols);
 #define MOE_PAIR_CASE(E_)                                                            \
   case E_:                                                                           \
     return bk2 ? launch_pair<E_, 2>(P, ma, mas, mb, mb3, mo, mo2, pair_tiles, psmem, s)   \

@@ -50,6 +50,7 @@
 #include "device_common.cuh"
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
+#include "tmem_share.h"
 
 #ifndef MOE_ROUTER_TC
 #define MOE_ROUTER_TC 1
@@ -605,8 +606,8 @@ RtShape rt_shape(const moe_config *c) {
   if (st < 2 || recv > avail) return r;
   r.stages = st;
   const size_t region = std::max((size_t)st * stage, recv);
-  // at least 120 KB: one CTA (and one 512-column TMEM allocation) an SM
-  r.smem = std::max<size_t>(1024 + region + hist, 120 * 1024);
+  // (one CTA, and one allocation of all TMEM columns, an SM)
+  r.smem = tmem_smem(1024 + region + hist, kTmemColumns);
   const int epl = ((c->E + kRtLanes - 1) / kRtLanes + 3) / 4 * 4;
   r.epl = epl < 4 ? 4 : epl;
   r.ok = true;
