@@ -32,9 +32,8 @@ constexpr uint32_t kWBytes = kFewWBytes;
 
 struct FewParams {
   CUtensorMap x, w, w3;
-  int64_t M;
-  int32_t N, KB;                 // k-blocks in all
-  int32_t tt;                    // tokens of a tile (the MMA's N)
+  int32_t M, N, KB;                 // k-blocks in all
+  int32_t tt;                    // tokens (the MMA's N): M rounded up to 16
   int32_t planes;                // of x: stacked on the MMA's N side, joined when the accumulator is read
   int32_t stages, split, tmem_cols, act;
   const void *bias, *bias3, *residual;
@@ -92,7 +91,6 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int split = P.split, rank = (int)(blockIdx.x % (unsigned)split);
   const int n0 = (int)(blockIdx.x / (unsigned)split) * BN;
-  const int64_t t0 = (int64_t)blockIdx.y * P.tt;
   const int kb0 = (int)((int64_t)P.KB * rank / split), kb1 = (int)((int64_t)P.KB * (rank + 1) / split);
 
   if (tid == 32) {
@@ -143,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
       mbar_expect_tx(&full_bar[stage], stage_bytes);
       tma_load_3d(s0, &P.w, fb, kb * BK, n0, 0);
       if (GATED) tma_load_3d(s0 + kWBytes, &P.w3, fb, kb * BK, n0, 0);
-      tma_load_3d(s0 + NW * kWBytes, &P.x, fb, kb * BK, (int)t0, 0);           // all planes
+      tma_load_3d(s0 + NW * kWBytes, &P.x, fb, kb * BK, 0, 0);                 // all planes
       if (++stage == P.stages) { stage = 0; phase ^= 1u; }
     }
     // aborting: the last round of each stage has to land before the exit
@@ -211,17 +209,16 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
     const bool in = n < P.N;
     const float b = in && P.bias ? to_f32(static_cast<const T *>(P.bias)[n]) : 0.0f;
     const float b3 = GATED && in && P.bias3 ? to_f32(static_cast<const T *>(P.bias3)[n]) : 0.0f;
-    const int nt = (int)min((int64_t)P.tt, P.M - t0);
     const uint32_t p0 = smem0 + 4u * row, m3 = (uint32_t)P.tt * BN * 4;
     // U tokens at a time, with everything they read in flight (a token past the
     // last one reads the last one again); partials of four ranks at a time,
     // added in rank order
-    for (int t = 2 * rank + tid / BN; t < nt; t += U * step) {
+    for (int t = 2 * rank + tid / BN; t < P.M; t += U * step) {
       float v[U] = {}, u[U] = {}, res[U] = {};
       if (!GATED && P.residual && in) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-          res[i] = to_f32(static_cast<const T *>(P.residual)[(t0 + min(t + i * step, nt - 1)) * P.ld_r + n]);
+          res[i] = to_f32(static_cast<const T *>(P.residual)[(int64_t)min(t + i * step, P.M - 1) * P.ld_r + n]);
       }
       for (int r = 0; r < split; r += 4) {
         float pv[4][U], pu[4][U];
@@ -231,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
           const uint32_t p = mapa_shared(p0, (uint32_t)(r + q));
 #pragma unroll
           for (int i = 0; i < U; ++i) {
-            const int ti = min(t + i * step, nt - 1);
+            const int ti = min(t + i * step, P.M - 1);
             pv[q][i] = ld_cluster_f32(p + (uint32_t)ti * BN * 4);
             if (GATED) pu[q][i] = ld_cluster_f32(p + m3 + (uint32_t)ti * BN * 4);
           }
@@ -247,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
         }
       }
       if (!in) continue;
-      const int live = (nt - 1 - t) / step + 1;               // tokens of these U that exist
+      const int live = (P.M - 1 - t) / step + 1;               // tokens of these U that exist
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         v[i] += b;
@@ -257,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < U; ++i)
           if (i < live) {
-            const int64_t at = (t0 + t + i * step) * P.N + n;
+            const int64_t at = (int64_t)(t + i * step) * P.N + n;
             from_f32(static_cast<T *>(P.pre)[at], v[i]);
             if (GATED && P.pre3) from_f32(static_cast<T *>(P.pre3)[at], u[i]);
           }
@@ -269,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const __grid_consta
 #pragma unroll
       for (int i = 0; i < U; ++i)
         if (i < live) {
-          T *o = static_cast<T *>(P.out) + (t0 + t + i * step) * P.ld_o + n;
+          T *o = static_cast<T *>(P.out) + (int64_t)(t + i * step) * P.ld_o + n;
           const float y = GATED ? v[i] * u[i] : v[i] + res[i];
           from_f32(*o, y);
           if (P.lo_stride) from_f32(o[P.lo_stride], rest_of(y, to_f32(*o)));
@@ -332,12 +329,12 @@ int64_t resident(int split, int per_sm) {
 }
 
 template <bool GATED, int U>
-cudaError_t launch_few_as(const FewParams &P, unsigned tiles, unsigned ttiles, size_t smem, cudaStream_t s) {
+cudaError_t launch_few_as(const FewParams &P, unsigned tiles, size_t smem, cudaStream_t s) {
   constexpr auto kern = dense_few_kernel<GATED, U>;
   cudaError_t e = allow_smem<kern>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * (unsigned)P.split, ttiles);
+  cfg.gridDim = dim3(tiles * (unsigned)P.split);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -377,7 +374,7 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   };
   if (!map(&P.x, g.a, g.M, P.tt) || !map(&P.w, g.b, g.N, BN) || (gated && !map(&P.w3, g.b3, g.N, BN)))
     return cudaErrorInvalidValue;
-  P.M = g.M;
+  P.M = (int32_t)g.M;
   P.N = g.N;
   P.act = g.act;
   P.bias = g.bias;
@@ -392,13 +389,13 @@ cudaError_t launch_dense_few(const DenseGemm &g, uint32_t *err, cudaStream_t s) 
   P.err = err;
   // a thread's tokens at a time: all of them, up to four (eight with one
   // matrix), so that their loads are in flight together; more would be idle loads
-  const unsigned nt = (unsigned)plan.tiles, tt = 1;
+  const unsigned nt = (unsigned)plan.tiles;
   const size_t smem = plan.smem;
   const int64_t each = (g.M + 2 * P.split - 1) / (2 * P.split);
-  if (each <= 1) return gated ? launch_few_as<true, 1>(P, nt, tt, smem, s) : launch_few_as<false, 1>(P, nt, tt, smem, s);
-  if (each <= 2) return gated ? launch_few_as<true, 2>(P, nt, tt, smem, s) : launch_few_as<false, 2>(P, nt, tt, smem, s);
-  if (gated) return launch_few_as<true, 4>(P, nt, tt, smem, s);
-  return each <= 4 ? launch_few_as<false, 4>(P, nt, tt, smem, s) : launch_few_as<false, 8>(P, nt, tt, smem, s);
+  if (each <= 1) return gated ? launch_few_as<true, 1>(P, nt, smem, s) : launch_few_as<false, 1>(P, nt, smem, s);
+  if (each <= 2) return gated ? launch_few_as<true, 2>(P, nt, smem, s) : launch_few_as<false, 2>(P, nt, smem, s);
+  if (gated) return launch_few_as<true, 4>(P, nt, smem, s);
+  return each <= 4 ? launch_few_as<false, 4>(P, nt, smem, s) : launch_few_as<false, 8>(P, nt, smem, s);
 }
 
 }  // namespace moe
