@@ -464,7 +464,7 @@ MOE_API moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const
 typedef struct moe_grad {
   const void *src;
   void *dst;
-  int64_t n;        /* >= 0                                                            */
+  int64_t n;        /* >= 0 (a list of more than 2^46 in all: MOE_ERR_UNSUPPORTED)     */
   int32_t dtype;    /* moe_dtype; a list may mix them                                  */
   int32_t reserved; /* 0                                                               */
 } moe_grad;

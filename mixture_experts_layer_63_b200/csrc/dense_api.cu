@@ -538,6 +538,11 @@ moe_status moe_gated_ffn_backward(const moe_gated_ffn_config *cfg, const void *x
 
 static moe_status validate_grads(const moe_grad *g, int32_t count, bool clip) {
   if (count < 0 || (count > 0 && !g)) return MOE_ERR_INVALID_ARG;
+  // beyond any memory, the byte counts here and the chunk counts of a launch
+  // (at least 2^16 elements each there): 2^46 elements in all
+  constexpr int64_t kMost = (int64_t)1 << 46;
+  int64_t total = 0;
+  bool large = false;
   for (int32_t i = 0; i < count; ++i) {
     if (g[i].n < 0 || g[i].reserved != 0 || (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16))
       return MOE_ERR_INVALID_ARG;
@@ -545,8 +550,10 @@ static moe_status validate_grads(const moe_grad *g, int32_t count, bool clip) {
     if (g[i].n > 0 && (!g[i].src || !aligned_to(g[i].src, es) ||
                        (clip && (!g[i].dst || !aligned_to(g[i].dst, es)))))
       return MOE_ERR_INVALID_ARG;
+    large = large || g[i].n > kMost - total;
+    if (!large) total += g[i].n;
   }
-  return MOE_OK;
+  return large ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 // In address order, what is written (dst and the norm) may not reach into the next piece.

@@ -1,5 +1,7 @@
 """The list of gradients that the binding hands to the C entry points, from
-whatever holds the tensors.  (Addresses and sizes only: no GPU.)"""
+whatever holds the tensors, and sizes that no memory holds.  (Addresses and
+sizes only: no GPU.)"""
+import ctypes
 import struct
 
 import pytest
@@ -46,3 +48,25 @@ def test_gradients_without_their_output_are_refused():
             api._grad_list(ts, out)
     # no gradient: no output asked for
     assert len(entries(api._grad_list([None, ts[0]], [None, ts[1]]))) == 1
+
+
+def test_sizes_beyond_any_memory_are_refused():
+    """... before their byte counts pass 64 bits or their chunk counts 32."""
+    from mixture_experts_layer_63_b200 import build
+    build.build()
+    L, need = api.lib(), ctypes.c_size_t(0)
+    assert L.moe_query_clip_size(300, ctypes.byref(need)) == api.MOE_OK
+    ws, norm = 1 << 60, 1 << 59
+    big = 1 << 46
+    for sizes in ([big + 1], [1 << 62], [(1 << 63) - 1], [3, big - 2], [1 << 62, 1 << 62, 1 << 62, 1 << 62],
+                  [big // 128] * 129):
+        for dt in (api.MOE_F32, api.MOE_BF16):
+            arr = (api.MoeGrad * len(sizes))()
+            for i, (e, n) in enumerate(zip(arr, sizes)):
+                e.src = e.dst = 256 * (i + 1)
+                e.n, e.dtype = n, dt
+            raw = bytes(arr)
+            assert L.moe_clip_grads(raw, len(sizes), 1.0, norm, ws, need.value, None) == api.MOE_ERR_UNSUPPORTED
+            assert L.moe_grad_norm(raw, len(sizes), norm, ws, need.value, None) == api.MOE_ERR_UNSUPPORTED
+            arr[0].n = -1                                # (a wrong entry is named first)
+            assert L.moe_grad_norm(bytes(arr), len(sizes), norm, ws, need.value, None) == api.MOE_ERR_INVALID_ARG
